@@ -26,6 +26,8 @@ BSP_SF_LAYOUT_128X4 = 0
 BSP_SF_LAYOUT_8X4 = 1
 BSP_NORM_RMS = 0
 BSP_NORM_LAYER = 1
+BSP_ACT_NONE, BSP_ACT_RELU, BSP_ACT_GELU, BSP_ACT_GELU_TANH, BSP_ACT_SILU = range(5)
+BSP_MAX_EXPERTS = 512
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 
@@ -68,6 +70,14 @@ SIGNATURES = {
     "nvfp4_gemm_ex": (_i32, [_vp, _vp, _i32, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _vp]),
     "mxfp8_quantize": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
     "mxfp8_gemm": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _i64, _vp]),
+    "nvfp4_gemm_fused": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _i32,
+                                _i64, _vp]),
+    "mxfp8_gemm_fused": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _i32, _i64,
+                                _vp]),
+    "nvfp4_grouped_gemm": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i32, _i32, _vp,
+                                  _i32, _i64, _vp]),
+    "mxfp8_grouped_gemm": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i32, _vp, _i32,
+                                  _i64, _vp]),
     "bsp_device_status": (_i32, [_vp]),
     "bsp_debug_encode_e2m1": (_i32, [_vp, _i64, _vp, _vp]),
     "bsp_debug_encode_e4m3": (_i32, [_vp, _i64, _vp, _vp]),

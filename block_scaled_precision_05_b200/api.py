@@ -20,6 +20,7 @@ Sources (page title, then symbol):
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 
 import torch
@@ -414,12 +415,112 @@ def _check_epilogue_args(alpha, row_scale, bias, N: int) -> None:
         raise TypeError(f"bias must be a contiguous bf16 tensor of {N} elements")
 
 
+ACTIVATIONS = {None: nat.BSP_ACT_NONE, "relu": nat.BSP_ACT_RELU, "gelu": nat.BSP_ACT_GELU,
+               "gelu_tanh": nat.BSP_ACT_GELU_TANH, "silu": nat.BSP_ACT_SILU}
+
+
+def interleave_gated(gate: torch.Tensor, up: torch.Tensor, dim: int = -2) -> torch.Tensor:
+    """The weight (or with dim=-1 the bias) of a gated pair of projections as
+    the gated GEMMs take it: rows gate 0, up 0, gate 1, up 1, ... along `dim`."""
+    if gate.shape != up.shape:
+        raise ValueError("gate and up must have the same shape")
+    d = dim % gate.dim()
+    return torch.stack((gate, up), dim=d + 1).flatten(d, d + 1)
+
+
+def _activation_code(activation: str | None) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    return ACTIVATIONS[activation]
+
+
+def _check_operand(what: str, codes: torch.Tensor, sf: torch.Tensor, shape: tuple, sf_bytes: int) -> None:
+    """A hand-made operand whose buffers are smaller than its sizes say would be read out of range."""
+    if codes.dtype != torch.uint8 or tuple(codes.shape) != shape or not codes.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous uint8 codes of shape {shape}, got {tuple(codes.shape)}")
+    if sf.dtype != torch.uint8 or sf.numel() != sf_bytes or not sf.is_contiguous():
+        raise ValueError(f"{what}: expected {sf_bytes} contiguous scale bytes, got {sf.numel()}")
+
+
+def _check_vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, shape: tuple) -> None:
+    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() != math.prod(shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {math.prod(shape)} elements {shape}")
+
+
+def _one_device(first: torch.Tensor, *ts: torch.Tensor | None) -> torch.device:
+    """The operands' device; the launch goes to that device's current stream."""
+    _require_cuda(first, *ts)
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"operands on different devices: {first.device} and {t.device}")
+    return first.device
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two row-major matrices of one shape and type share an element."""
+    lo_a, lo_b, size = a.data_ptr(), b.data_ptr(), a.element_size()
+    span = lambda t: ((t.shape[0] - 1) * t.stride(0) + t.shape[1]) * size  # noqa: E731
+    if a.numel() == 0 or lo_a >= lo_b + span(b) or lo_b >= lo_a + span(a):
+        return False
+    if a.stride(0) != b.stride(0):
+        return True
+    gap, ld = (lo_b - lo_a) // size, a.stride(0)
+    return gap % ld < a.shape[1] or -gap % ld < a.shape[1]  # column ranges modulo the common row stride
+
+
+def _gemm_fused(fp4: bool, a, b, alpha, row_scale, bias, out_dtype, out, activation, gated, residual) -> torch.Tensor:
+    """nvfp4_gemm / mxfp8_gemm with an activation, a gate or a residual."""
+    act = _activation_code(activation)
+    acodes, bcodes = (a.codes, b.codes) if fp4 else (a.q, b.q)
+    M, N, K = a.rows, b.rows, a.K
+    if gated and N % 2 != 0:
+        raise ValueError("a gated weight has an even number of rows")
+    dev = _one_device(acodes, a.sf, bcodes, b.sf, alpha, row_scale, bias, residual, out)
+    cols = N // 2 if gated else N
+    out, d_dtype = _out(M, cols, out_dtype, dev, out)
+    if residual is not None:
+        if residual.dtype != out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
+            raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
+        same = residual.data_ptr() == out.data_ptr() and residual.stride(0) == out.stride(0)
+        if not same and _overlap(residual, out):
+            raise ValueError("residual may be the output itself, but must not overlap it otherwise")
+    _check_epilogue_args(alpha, row_scale, bias, N)
+    _check_vector("alpha", alpha, torch.float32, (1,))
+    _check_vector("row_scale", row_scale, torch.float32, (M,))
+    width, sf_bytes = (K // 2, nvfp4_sf_bytes) if fp4 else (K, mxfp8_sf_bytes)
+    _check_operand("A", acodes, a.sf, (M, width), sf_bytes(M, K))
+    _check_operand("B", bcodes, b.sf, (N, width), sf_bytes(N, K))
+    tail = [act, int(gated), _ptr(residual), residual.stride(0) if residual is not None else 0, _ptr(out), d_dtype,
+            out.stride(0)]
+    with torch.cuda.device(dev):
+        head = [_ptr(acodes), _ptr(a.sf), _ptr(bcodes), _ptr(b.sf), M, N, K, _ptr(alpha)]
+        if fp4:
+            st = nat.lib().nvfp4_gemm_fused(*head, _ptr(row_scale), _ptr(bias), *tail, _stream())
+        else:
+            st = nat.lib().mxfp8_gemm_fused(*head, _ptr(bias), *tail, _stream())
+    nat.check(st, "nvfp4_gemm_fused" if fp4 else "mxfp8_gemm_fused")
+    return out
+
+
 def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, alpha: torch.Tensor | None = None,
                row_scale: torch.Tensor | None = None, bias: torch.Tensor | None = None,
-               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
-    """D = alpha * row_scale[m] * (A (x) sfA)(B (x) sfB)^T + bias, fp32 accumulate."""
+               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+               activation: str | None = None, gated: bool = False,
+               residual: torch.Tensor | None = None) -> torch.Tensor:
+    """D = act(y) + residual, y = alpha * row_scale[m] * (A (x) sfA)(B (x) sfB)^T
+    + bias, fp32 accumulate, one rounding.
+
+    activation: None, "relu", "gelu" (erf), "gelu_tanh" or "silu".  gated: the
+    rows of B alternate between a gate and an up projection (interleave_gated)
+    and D[m, j] = act(y[m, 2j]) * y[m, 2j + 1] + residual[m, j].  residual: of
+    D's shape and dtype; it may be `out` itself.  With any of them A's scales
+    are in the 128x4 layout."""
     if a.K != b.K:
         raise ValueError("A and B disagree on K")
+    if activation is not None or gated or residual is not None:
+        if a.sf_layout != "128x4" or b.sf_layout != "128x4":
+            raise ValueError("an activation, a gate or a residual needs scales in the 128x4 layout")
+        return _gemm_fused(True, a, b, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
     _require_cuda(a.codes, b.codes, alpha, row_scale, bias)
     M, N = a.rows, b.rows
     _check_epilogue_args(alpha, row_scale, bias, N)
@@ -435,10 +536,14 @@ def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, alpha: torch.Tensor | None = None
 
 def mxfp8_gemm(a: MXFP8Tensor, b: MXFP8Tensor, alpha: torch.Tensor | None = None,
                bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
-               out: torch.Tensor | None = None) -> torch.Tensor:
-    """D = alpha * (A (x) 2^sA)(B (x) 2^sB)^T + bias, fp32 accumulate."""
+               out: torch.Tensor | None = None, activation: str | None = None, gated: bool = False,
+               residual: torch.Tensor | None = None) -> torch.Tensor:
+    """D = act(y) + residual, y = alpha * (A (x) 2^sA)(B (x) 2^sB)^T + bias, fp32
+    accumulate; activation, gated and residual as in nvfp4_gemm."""
     if a.K != b.K:
         raise ValueError("A and B disagree on K")
+    if activation is not None or gated or residual is not None:
+        return _gemm_fused(False, a, b, alpha, None, bias, out_dtype, out, activation, gated, residual)
     _require_cuda(a.q, b.q, alpha, bias)
     M, N = a.rows, b.rows
     _check_epilogue_args(alpha, None, bias, N)
@@ -447,6 +552,137 @@ def mxfp8_gemm(a: MXFP8Tensor, b: MXFP8Tensor, alpha: torch.Tensor | None = None
                               _ptr(out), d_dtype, out.stride(0), _stream())
     nat.check(st, "mxfp8_gemm")
     return out
+
+
+# --------------------------------------------------------------------------- grouped by expert
+@dataclass
+class NVFP4Experts:
+    """Stacked NVFP4 weights: codes uint8 [E, N, K/2], scales uint8
+    [E, nvfp4_sf_bytes(N, K)] (each expert's in 128x4 tiles of its own)."""
+    codes: torch.Tensor
+    sf: torch.Tensor
+    K: int
+
+    @property
+    def experts(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[1]
+
+
+@dataclass
+class MXFP8Experts:
+    """Stacked MXFP8 weights: e4m3 bytes [E, N, K], e8m0 scales uint8
+    [E, mxfp8_sf_bytes(N, K)]."""
+    q: torch.Tensor
+    sf: torch.Tensor
+    K: int
+
+    @property
+    def experts(self) -> int:
+        return self.q.shape[0]
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[1]
+
+
+def _check_expert_weight(w: torch.Tensor) -> torch.Tensor:
+    _require_cuda(w)
+    if w.dim() != 3 or w.shape[0] < 1 or w.shape[1] < 1 or w.shape[2] < 32 or w.shape[2] % 32 != 0:
+        raise ValueError(f"expects weights [E, N, K] with K % 32 == 0, got {tuple(w.shape)}")
+    if w.shape[0] > nat.BSP_MAX_EXPERTS:
+        raise ValueError(f"at most {nat.BSP_MAX_EXPERTS} experts, got {w.shape[0]}")
+    return w
+
+
+def nvfp4_quantize_experts(w: torch.Tensor, fp8_fp4_max: float = FP8_FP4_MAX):
+    """Load-time conversion of stacked bf16 or fp16 weights [E, N, K], each
+    expert with a global scale of its own from its amax.  Returns
+    (NVFP4Experts, gs [E], 1/gs [E])."""
+    w = _check_expert_weight(coerce_input(w)).contiguous()
+    E, N, K = w.shape
+    q = NVFP4Experts(torch.empty((E, N, K // 2), dtype=torch.uint8, device=w.device),
+                     torch.empty((E, nvfp4_sf_bytes(N, K)), dtype=torch.uint8, device=w.device), K)
+    gs, inv = (torch.empty(E, dtype=torch.float32, device=w.device) for _ in range(2))
+    with torch.cuda.device(w.device):
+        for e in range(E):
+            s, i = nvfp4_global_scale(amax(w[e]), fp8_fp4_max)
+            nvfp4_quantize(w[e], s, out=NVFP4Tensor(q.codes[e], q.sf[e], K))
+            gs[e:e + 1].copy_(s)
+            inv[e:e + 1].copy_(i)
+    return q, gs, inv
+
+
+def mxfp8_quantize_experts(w: torch.Tensor) -> MXFP8Experts:
+    """Stacked bf16 weights [E, N, K] to MXFP8."""
+    w = _check_expert_weight(coerce_bf16(w)).contiguous()
+    E, N, K = w.shape
+    q = MXFP8Experts(torch.empty((E, N, K), dtype=torch.uint8, device=w.device),
+                     torch.empty((E, mxfp8_sf_bytes(N, K)), dtype=torch.uint8, device=w.device), K)
+    with torch.cuda.device(w.device):
+        for e in range(E):
+            mxfp8_quantize(w[e], out=MXFP8Tensor(q.q[e], q.sf[e], K))
+    return q
+
+
+def _grouped_gemm(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated):
+    if a.K != b.K:
+        raise ValueError("A and B disagree on K")
+    act = _activation_code(activation)
+    acodes, bcodes = (a.codes, b.codes) if fp4 else (a.q, b.q)
+    M, E, N, K = a.rows, b.experts, b.rows, a.K
+    if E < 1 or E > nat.BSP_MAX_EXPERTS:
+        raise ValueError(f"1 to {nat.BSP_MAX_EXPERTS} experts, got {E}")
+    if gated and N % 2 != 0:
+        raise ValueError("a gated weight has an even number of rows")
+    dev = _one_device(acodes, a.sf, bcodes, b.sf, offsets, alpha, row_scale, bias, out)
+    if offsets is None or offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 tensor of {E + 1} elements")
+    width, sf_bytes = (K // 2, nvfp4_sf_bytes) if fp4 else (K, mxfp8_sf_bytes)
+    _check_operand("A", acodes, a.sf, (M, width), sf_bytes(M, K))
+    _check_operand("B", bcodes, b.sf, (E, N, width), E * sf_bytes(N, K))
+    _check_vector("alpha", alpha, torch.float32, (E,))
+    _check_vector("row_scale", row_scale, torch.float32, (M,))
+    _check_vector("bias", bias, torch.bfloat16, (E, N))
+    out, d_dtype = _out(M, N // 2 if gated else N, out_dtype, dev, out)
+    with torch.cuda.device(dev):
+        head = [_ptr(acodes), _ptr(a.sf), _ptr(bcodes), _ptr(b.sf), _ptr(offsets), E, M, N, K, _ptr(alpha)]
+        tail = [_ptr(bias), act, int(gated), _ptr(out), d_dtype, out.stride(0), _stream()]
+        if fp4:
+            st = nat.lib().nvfp4_grouped_gemm(*head, _ptr(row_scale), *tail)
+        else:
+            st = nat.lib().mxfp8_grouped_gemm(*head, *tail)
+    nat.check(st, "nvfp4_grouped_gemm" if fp4 else "mxfp8_grouped_gemm")
+    return out
+
+
+def nvfp4_grouped_gemm(a: NVFP4Tensor, b: NVFP4Experts, offsets: torch.Tensor, alpha: torch.Tensor | None = None,
+                       row_scale: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                       activation: str | None = None, gated: bool = False) -> torch.Tensor:
+    """Each expert's weight times its own rows of A, in one launch without a
+    host sync: for offsets[e] <= m < offsets[e + 1]
+    y = alpha[e] * row_scale[m] * (A (x) sfA)(B[e] (x) sfB[e])^T + bias[e], and D
+    from y by `activation` and `gated` as in nvfp4_gemm.
+
+    A's rows are the experts' tokens one expert after another, quantized as one
+    [M, K] activation; offsets int32 [E + 1] on the device; alpha fp32 [E], bias
+    bf16 [E, N].  Rows outside every expert keep what `out` held (without `out`
+    they are undefined)."""
+    if a.sf_layout != "128x4":
+        raise ValueError("the grouped GEMM needs activation scales in the 128x4 layout")
+    return _grouped_gemm(True, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated)
+
+
+def mxfp8_grouped_gemm(a: MXFP8Tensor, b: MXFP8Experts, offsets: torch.Tensor, alpha: torch.Tensor | None = None,
+                       bias: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                       out: torch.Tensor | None = None, activation: str | None = None,
+                       gated: bool = False) -> torch.Tensor:
+    """nvfp4_grouped_gemm for MXFP8 operands."""
+    return _grouped_gemm(False, a, b, offsets, alpha, None, bias, out_dtype, out, activation, gated)
 
 
 def device_status() -> int:
@@ -513,14 +749,18 @@ class NVFP4Linear:
                                         per_row=self.per_token)
 
     def __call__(self, x: torch.Tensor, pre_quantized: NVFP4Tensor | None = None,
-                 out_dtype: torch.dtype = torch.bfloat16, sf_layout: str = "128x4") -> torch.Tensor:
+                 out_dtype: torch.dtype = torch.bfloat16, sf_layout: str = "128x4", activation: str | None = None,
+                 gated: bool = False, residual: torch.Tensor | None = None) -> torch.Tensor:
         """sf_layout "8x4": the activation's scales in 8-row tiles (mm_fp4's
-        use_8x4_sf_layout), for at most 64 rows."""
+        use_8x4_sf_layout), for at most 64 rows.  activation, gated, residual:
+        fused into the GEMM (nvfp4_gemm); residual [..., out columns] of
+        out_dtype."""
         lead = x.shape[:-1]
         xq = pre_quantized if pre_quantized is not None else self.quantize_input(x, sf_layout)
         y = nvfp4_gemm(xq, self.weight, self.alpha, xq.row_inv_gs if self.per_token else None, self.bias,
-                       out_dtype=out_dtype)
-        return y.view(*lead, self.out_features)
+                       out_dtype=out_dtype, activation=activation, gated=gated,
+                       residual=None if residual is None else _as_2d(residual))
+        return y.view(*lead, y.shape[1])
 
 
     @classmethod
@@ -549,7 +789,62 @@ class MXFP8Linear:
         self.weight = mxfp8_quantize(w)
         self.bias = None if bias is None else coerce_bf16(bias).contiguous()
 
-    def __call__(self, x: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor, out_dtype: torch.dtype = torch.bfloat16, activation: str | None = None,
+                 gated: bool = False, residual: torch.Tensor | None = None) -> torch.Tensor:
+        """activation, gated, residual: as in NVFP4Linear."""
         lead = x.shape[:-1]
         xq = mxfp8_quantize(coerce_bf16(x))
-        return mxfp8_gemm(xq, self.weight, None, self.bias, out_dtype=out_dtype).view(*lead, self.out_features)
+        y = mxfp8_gemm(xq, self.weight, None, self.bias, out_dtype=out_dtype, activation=activation, gated=gated,
+                       residual=None if residual is None else _as_2d(residual))
+        return y.view(*lead, y.shape[1])
+
+
+class NVFP4GroupedLinear:
+    """The experts of a mixture as one W4A4 NVFP4 linear layer: weights [E, N, K]
+    quantized once, each with its own global scale; a call quantizes the tokens
+    (sorted by expert) and runs every expert's product in one launch.
+
+    bias [E, N]; per_token and four_over_six as in NVFP4Linear; activation and
+    gated are fused into the product (gated: interleave_gated(w1, w3))."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, per_token: bool = False,
+                 four_over_six: bool = False, activation: str | None = None, gated: bool = False):
+        _activation_code(activation)
+        self.weight, self.gs_w, self.inv_gs_w = nvfp4_quantize_experts(
+            weight, FP8_FP4_MAX_4OVER6 if four_over_six else FP8_FP4_MAX)
+        self.experts, self.in_features = weight.shape[0], weight.shape[2]
+        self.out_features = weight.shape[1] // 2 if gated else weight.shape[1]
+        self.per_token, self.activation, self.gated = per_token, activation, gated
+        self.gs_x = torch.ones(1, dtype=torch.float32, device=weight.device)
+        # the static activation scale is 1, so alpha = 1 / (gs_x gs_w) = 1 / gs_w either way
+        self.alpha = self.inv_gs_w
+        self.bias = None if bias is None else coerce_bf16(bias).contiguous()
+
+    def quantize_input(self, x: torch.Tensor) -> NVFP4Tensor:
+        return nvfp4_quantize(coerce_input(x), None if self.per_token else self.gs_x, per_row=self.per_token)
+
+    def __call__(self, x: torch.Tensor | None, offsets: torch.Tensor, pre_quantized: NVFP4Tensor | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+        """x [M, K], or its quantized form as pre_quantized; offsets int32 [E + 1]."""
+        xq = pre_quantized if pre_quantized is not None else self.quantize_input(x)
+        return nvfp4_grouped_gemm(xq, self.weight, offsets, self.alpha, xq.row_inv_gs if self.per_token else None,
+                                  self.bias, out_dtype, out, self.activation, self.gated)
+
+
+class MXFP8GroupedLinear:
+    """NVFP4GroupedLinear in W8A8 MXFP8."""
+
+    def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
+                 gated: bool = False):
+        _activation_code(activation)
+        self.weight = mxfp8_quantize_experts(weight)
+        self.experts, self.in_features = weight.shape[0], weight.shape[2]
+        self.out_features = weight.shape[1] // 2 if gated else weight.shape[1]
+        self.activation, self.gated = activation, gated
+        self.bias = None if bias is None else coerce_bf16(bias).contiguous()
+
+    def __call__(self, x: torch.Tensor | None, offsets: torch.Tensor, pre_quantized: MXFP8Tensor | None = None,
+                 out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+        xq = pre_quantized if pre_quantized is not None else mxfp8_quantize(coerce_bf16(x))
+        return mxfp8_grouped_gemm(xq, self.weight, offsets, None, self.bias, out_dtype, out, self.activation,
+                                  self.gated)

@@ -67,6 +67,7 @@
 // the CTA drains its outstanding copies and MMAs, frees tensor memory and exits.
 #include "bsp_device.cuh"
 #include "bsp_internal.h"
+#include "tensor_maps.h"
 
 // Tuning knobs (compile-time): pipeline depth, and how the epilogue writes D --
 // 1: 32x32-byte swizzled shared-memory staging + TMA stores, with
@@ -110,8 +111,6 @@
 
 namespace bsp {
 namespace {
-
-enum Kind : int { kNVF4 = 0, kMXF8 = 1 };
 
 constexpr int64_t kSf8MaxM = 64;  // rows of an activation whose scales may be in the 8x4 layout
 
@@ -195,11 +194,6 @@ __device__ __forceinline__ void tile_coords(int t, int num_m, int num_n, int G, 
   const int r = t - g * per_group;
   mb = first + r % gsz;
   nb = r / gsz;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <int KIND, int BN, int CG>
@@ -1056,11 +1050,6 @@ __global__ void __launch_bounds__(SkCfg<KIND, BNA, kSf8, kSplit>::THREADS, 1)
   }
 }
 
-int encode_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows,
-                   int box_bytes = 128);
-int encode_scales(CUtensorMap* m, const void* base, int64_t bands, int64_t tiles_per_band, int atoms, int box_bands);
-int encode_rows_plain(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows, int box_bytes);
-
 template <int KIND, int BNA, bool kSf8 = false, bool kSplit = false>
 int launch_skinny(const DeviceInfo& dev, const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
                   int64_t row_bytes, int64_t tiles_per_band, GemmParams p, cudaStream_t stream) {
@@ -1141,59 +1130,6 @@ int launch_skinny_any(const DeviceInfo& dev, const uint8_t* A, const uint8_t* sf
   if (p.split > 1)
     return launch_skinny<KIND, BNA, kSf8, true>(dev, A, sfA, B, sfB, row_bytes, tiles_per_band, p, stream);
   return launch_skinny<KIND, BNA, kSf8, false>(dev, A, sfA, B, sfB, row_bytes, tiles_per_band, p, stream);
-}
-
-// Row-major uint8 matrix [rows, row_bytes], boxes of box_rows x box_bytes (128
-// or 64) with the matching TMA swizzle.
-int encode_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows, int box_bytes) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t es[2] = {1u, 1u};
-  CUresult r = encode_tiled_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                 box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
-}
-
-// Row-major bytes [rows, row_bytes], boxes of box_rows x box_bytes, no swizzle.
-int encode_rows_plain(CUtensorMap* m, const void* base, int64_t rows, int64_t row_bytes, int box_rows, int box_bytes) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t es[2] = {1u, 1u};
-  CUresult r = encode_tiled_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
-}
-
-// Tile-mapped scale buffer viewed as [bands][tiles per band][512 bytes] with
-// 8-byte elements; a box covers `atoms` consecutive 512-byte tiles of `bands`
-// consecutive row bands.
-int encode_scales(CUtensorMap* m, const void* base, int64_t bands, int64_t tiles_per_band, int atoms, int box_bands) {
-  cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(tiles_per_band), static_cast<cuuint64_t>(bands)};
-  cuuint64_t strides[2] = {512u, static_cast<cuuint64_t>(tiles_per_band * 512)};
-  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(atoms), static_cast<cuuint32_t>(box_bands)};
-  cuuint32_t es[3] = {1u, 1u, 1u};
-  CUresult r = encode_tiled_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, 3, const_cast<void*>(base), dims, strides, box, es,
-                                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
-}
-
-// Row-major output [rows, ld] of bf16 or fp32, boxes of 32 rows x 32 bytes, 32-byte swizzle.
-int encode_output(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
-  const int64_t esize = f32 ? 4 : 2;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * esize)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(32 / esize), 32u};
-  cuuint32_t es[2] = {1u, 1u};
-  CUresult r = encode_tiled_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
-                                 dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
 }
 
 template <int KIND, int BN, int CG = 1>

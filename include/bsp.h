@@ -82,6 +82,18 @@ enum {
     BSP_SF_LAYOUT_8X4 = 1
 };
 
+/* Activations of the fused GEMM epilogues (fp32, before the one rounding of the output). */
+enum {
+    BSP_ACT_NONE = 0,
+    BSP_ACT_RELU = 1,      /* max(y, 0) */
+    BSP_ACT_GELU = 2,      /* y * Phi(y), Phi the normal distribution function (the erf form) */
+    BSP_ACT_GELU_TANH = 3, /* y/2 * (1 + tanh(sqrt(2/pi) * (y + 0.044715 y^3))) */
+    BSP_ACT_SILU = 4       /* y / (1 + e^-y) */
+};
+
+/* Most experts of a grouped GEMM. */
+#define BSP_MAX_EXPERTS 512
+
 /* Norms of the fused norm + quantize producers (bsp_debug_norm_stats). */
 enum {
     BSP_NORM_RMS = 0,
@@ -424,6 +436,60 @@ int mxfp8_quantize(const uint16_t *x, int64_t M, int64_t K, int64_t ld_x,
 int mxfp8_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
                int64_t M, int64_t N, int64_t K, const float *alpha,
                const uint16_t *bias, void *D, int d_dtype, int64_t ld_d, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * GEMMs with a fused epilogue: a linear layer's activation (and the product
+ * of a gated pair of projections) and the residual it is added to, in one
+ * launch with the GEMM.
+ *   y[m, n] = alpha * row_scale[m] * sum_k A(m,k) sA B(n,k) sB + bias[n]
+ *   gated == 0: D[m, n] = act(y[m, n]) + residual[m, n]
+ *   gated == 1: D[m, j] = act(y[m, 2j]) * y[m, 2j+1] + residual[m, j]
+ * All of it in fp32, rounded once to the output type.
+ *   A, sfA, B, sfB, alpha, row_scale, bias, D, d_dtype: as nvfp4_gemm /
+ *              mxfp8_gemm.  gated: B's rows (and bias) alternate between the
+ *              gate and the up projection, D has N/2 columns
+ *   activation: BSP_ACT_*
+ *   residual : [M, N or N/2] of D's element type, row stride ld_residual, or
+ *              NULL.  It may be D itself (same pointer and stride); otherwise
+ *              the two do not overlap.
+ * Errors as nvfp4_gemm; an unknown activation, gated not 0 or 1, gated with
+ * N % 16 != 0, or ld_residual below the columns of D -> INVALID_ARG;
+ * a residual or ld_residual off 16 bytes -> ALIGNMENT. */
+int nvfp4_gemm_fused(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
+                     int64_t M, int64_t N, int64_t K, const float *alpha, const float *row_scale,
+                     const uint16_t *bias, int activation, int gated, const void *residual,
+                     int64_t ld_residual, void *D, int d_dtype, int64_t ld_d, bsp_stream_t stream);
+int mxfp8_gemm_fused(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
+                     int64_t M, int64_t N, int64_t K, const float *alpha, const uint16_t *bias,
+                     int activation, int gated, const void *residual, int64_t ld_residual, void *D,
+                     int d_dtype, int64_t ld_d, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * GEMMs grouped by expert: each expert's weight times its own rows of A, every
+ * expert in one launch.  The rows of A are the experts' tokens one expert after
+ * another, without padding; A and sfA are what the quantizers write for the
+ * whole [M, K] activation.  For each expert e and offsets[e] <= m < offsets[e+1]:
+ *   y[m, n] = alpha[e] * row_scale[m] * sum_k A(m,k) sA B[e](n,k) sB[e] + bias[e, n]
+ * and D from y as in the fused epilogue above (no residual).  Rows outside
+ * every expert are left as they were.
+ *   B       : codes [E, N, K/2] (NVFP4) or [E, N, K] (MXFP8), dense
+ *   sfB     : E scale buffers of bsp_nvfp4_sf_bytes(N, K) / bsp_mxfp8_sf_bytes(N, K)
+ *             bytes one after another (each expert quantized by itself)
+ *   offsets : int32 [E + 1] on the device.  Values outside [0, M] are clamped,
+ *             and one below an earlier one counts as that one.  An expert may
+ *             have no row.
+ *   alpha   : fp32 [E] or NULL (1);  row_scale : fp32 [M] or NULL
+ *   bias    : bf16 [E, N] or NULL
+ * Errors as above; E outside 1 .. BSP_MAX_EXPERTS, or no offsets -> INVALID_ARG. */
+int nvfp4_grouped_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
+                       const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                       const float *alpha, const float *row_scale, const uint16_t *bias,
+                       int activation, int gated, void *D, int d_dtype, int64_t ld_d,
+                       bsp_stream_t stream);
+int mxfp8_grouped_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
+                       const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
+                       const float *alpha, const uint16_t *bias, int activation, int gated, void *D,
+                       int d_dtype, int64_t ld_d, bsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device error word.
