@@ -58,28 +58,13 @@ __device__ __forceinline__ float act_gelu(float x) {
   return fmaf(-u * ex2_approx(-0.72134752f * u * u), p, act_relu(x));
 }
 
-// Applies the activation to every `kStep`-th of N values; the switch is uniform over the launch.
-template <int N, int kStep>
-__device__ __forceinline__ void activate(float (&y)[N], int act) {
-  switch (act) {
-    case BSP_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < N; i += kStep) y[i] = act_relu(y[i]);
-      break;
-    case BSP_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < N; i += kStep) y[i] = act_gelu(y[i]);
-      break;
-    case BSP_ACT_GELU_TANH:
-#pragma unroll
-      for (int i = 0; i < N; i += kStep) y[i] = act_gelu_tanh(y[i]);
-      break;
-    case BSP_ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < N; i += kStep) y[i] = act_silu(y[i]);
-      break;
-    default: break;
-  }
+template <int ACT>
+__device__ __forceinline__ float activate(float y) {
+  if constexpr (ACT == BSP_ACT_RELU) return act_relu(y);
+  else if constexpr (ACT == BSP_ACT_GELU) return act_gelu(y);
+  else if constexpr (ACT == BSP_ACT_GELU_TANH) return act_gelu_tanh(y);
+  else if constexpr (ACT == BSP_ACT_SILU) return act_silu(y);
+  else return y;
 }
 
 }  // namespace bsp

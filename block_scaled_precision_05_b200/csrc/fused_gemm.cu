@@ -29,14 +29,14 @@
 namespace bsp {
 namespace {
 
-constexpr int kMaxExperts = BSP_MAX_EXPERTS;  // the tile table's three words per expert in shared memory
+constexpr int kMaxExperts = BSP_MAX_EXPERTS;  // the tile table's two words per expert in shared memory
 
 struct FusedParams {
   int M, N, E;
   int num_kb;     // 128-byte steps of K
   int panels;     // weight panels per expert
   int group_m;    // token tiles per rasterisation group
-  int act, gated, out_f32;
+  int act, gated;
   const int32_t* offsets;  // [E + 1], or NULL: one expert with every row
   const float* alpha;
   const float* row_scale;
@@ -55,7 +55,7 @@ struct FCfg {
   static constexpr int TN = CG == 2 ? 256 : 64;          // most tokens per tile
   static constexpr int N_STEP = CG == 2 ? 32 : 16;       // granularity of the MMA's N
   static constexpr int X_ROWS = TN / CG;                 // token rows each CTA holds
-  static constexpr int X_BOX = 32;                       // rows per TMA box of tokens
+  static constexpr int X_MAPS = X_ROWS / 32;             // sizes of the TMA box of tokens
   static constexpr int ATOMS = KIND == kNVF4 ? 4 : 1;    // 128x4 scale tiles per 128 rows per stage
   static constexpr int X_BANDS = CG == 2 ? 3 : 2;        // bands of scale tiles that TN rows at any offset touch
   static constexpr int X_WORDS = CG == 2 ? 8 : 4;        // scale columns per K-group tile
@@ -73,17 +73,15 @@ struct FCfg {
   static constexpr int EPI_WARPS = CG == 2 ? 8 : 4;
   static constexpr int FIRST_SF_WARP = 4, FIRST_EPI_WARP = 8;
   static constexpr int THREADS = (8 + EPI_WARPS) * 32;
-  static constexpr int CHUNKS = TN / (EPI_WARPS / 4) / 16;  // 16-token chunks per epilogue warp
+  static constexpr int STEPS = TN / (EPI_WARPS / 4) / 16;  // steps of 16 tokens per epilogue warp
   // CTA pairs: warpgroups 0 and 1 hand registers to the epilogue, which holds 128 accumulator columns a thread
   static constexpr int WG0_REGS = 40, SF_REGS = 88, EPI_REGS = 192;
   static_assert(CG == 1 || 128 * (WG0_REGS + SF_REGS + 2 * EPI_REGS) == THREADS * (65536 / THREADS), "register split");
-  // staging: 16 tokens x 32 weight rows of fp32 per warp, rows padded to 36 words so that 16-byte reads of 8 lanes
-  // (two tokens x four 8-column segments) touch every bank once
-  static constexpr int STG_LD = 36;
-  static constexpr int STG_BYTES = 16 * STG_LD * 4;
-  static constexpr int TABLE_BYTES = ((3 * kMaxExperts + 1) * 4 + 15) / 16 * 16;
+  static constexpr int STG_BYTES = 1024;  // staging: two buffers per warp, each a box of D for one TMA store
+  static constexpr int SCALE_BYTES = 16 * STEPS * 4;  // and its tokens' scales
+  static constexpr int TABLE_BYTES = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int FIXED_BYTES = EPI_WARPS * STG_BYTES + TABLE_BYTES + BAR_BYTES + 1024;
+  static constexpr int FIXED_BYTES = EPI_WARPS * (2 * STG_BYTES + SCALE_BYTES) + TABLE_BYTES + BAR_BYTES + 1024;
   static constexpr int by_smem = (232448 - FIXED_BYTES) / STAGE_BYTES;
   static constexpr int by_tmem = (TMEM_COLS - ACC_COLS) / SF_COLS;
   static constexpr int STAGES = by_smem < by_tmem ? (by_smem < 8 ? by_smem : 8) : (by_tmem < 8 ? by_tmem : 8);
@@ -91,6 +89,18 @@ struct FCfg {
   static_assert(STAGES >= 4 && SMEM_BYTES <= 232448 && ACC_COLS + STAGES * SF_COLS <= TMEM_COLS, "budget");
   static_assert((4 * STAGES + 8) * 8 <= BAR_BYTES, "barrier space");
 };
+
+// TMA descriptors.  Tokens and their scales come in one box each per stage, of the smallest size that covers the
+// tile: x[i] has 32 (i + 1) rows, sfx[i] has i + 1 bands.  (A loop over small boxes in the producer thread took 0.2 us
+// per stage: 14.2 instead of 10.4 us at M = 16, N = 13824, K = 5120.)
+struct FusedMaps {
+  CUtensorMap w, sfw, x[4], sfx[3], d;
+};
+
+// Gated weights: accumulator row 16 b + j holds the gate of output column 8 b + j, row 16 b + 8 + j its up projection
+// (j < 8), so that a thread of the epilogue has both.  The TMA load reorders the rows (a box of 8 rows two apart, both
+// kinds, 8 blocks); this is the weight's row in accumulator row r.
+__device__ __forceinline__ int gated_row(int r) { return (r & ~15) + 2 * (r & 7) + ((r >> 3) & 1); }
 
 struct Tile {
   int e;      // expert
@@ -100,16 +110,14 @@ struct Tile {
   int nmma;   // rows rounded up to the MMA's granularity
 };
 
-// The experts' tiles: start[e] is the index of expert e's first tile, rows lo[e] <= m < hi[e].
+// The experts' tiles: start[e] is the index of expert e's first tile, its rows are lo[e] <= m < lo[e + 1].
 struct Table {
   int* start;
   int* lo;
-  int* hi;
 
   __device__ __forceinline__ void carve(void* mem) {
     start = static_cast<int*>(mem);
     lo = start + kMaxExperts + 1;
-    hi = lo + kMaxExperts;
   }
 
   // Offsets are clamped to [0, M], and one below an earlier one counts as that one, so that the experts' rows never
@@ -119,21 +127,21 @@ struct Table {
     if (p.offsets == nullptr) {
       if (threadIdx.x == 0) {
         lo[0] = 0;
-        hi[0] = p.M;
+        lo[1] = p.M;
         start[0] = 0;
         start[1] = (p.M + TN - 1) / TN * p.panels;
       }
       return;
     }
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) hi[e] = min(max(__ldg(p.offsets + e + 1), 0), p.M);
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) lo[e] = min(max(__ldg(p.offsets + e), 0), p.M);
     __syncthreads();
     if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
-      int top = min(max(__ldg(p.offsets), 0), p.M);  // the rows before this expert
+      int top = lo[0];  // the rows before this expert
       int tiles = 0;
       for (int e0 = 0; e0 < p.E; e0 += 32) {
         const int e = e0 + lane;
-        int h = e < p.E ? hi[e] : 0;
+        int h = e < p.E ? lo[e + 1] : 0;
         h = max(h, top);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -150,8 +158,7 @@ struct Table {
           if (lane >= d) n += o;
         }
         if (e < p.E) {
-          lo[e] = l;
-          hi[e] = h;
+          lo[e + 1] = h;
           start[e] = tiles + n - own;
         }
         top = __shfl_sync(0xFFFFFFFFu, h, 31);
@@ -171,7 +178,7 @@ struct Table {
       if (start[mid] <= t) a = mid;
       else b = mid;
     }
-    const int l = lo[a], rows = hi[a] - l;
+    const int l = lo[a], rows = lo[a + 1] - l;
     const int nt = (rows + TN - 1) / TN;
     const int r = t - start[a];
     const int per_group = p.group_m * p.panels;
@@ -186,22 +193,87 @@ struct Table {
     q.e = a;
     q.nb = nb;
     q.row0 = l + mt * per;
-    q.cnt = min(per, hi[a] - q.row0);
+    q.cnt = min(per, l + rows - q.row0);
     q.nmma = (q.cnt + N_STEP - 1) / N_STEP * N_STEP;
     return q;
   }
 };
 
-template <int KIND, int CG>
+__device__ __forceinline__ void lds16(uint32_t* r, const uint8_t* p) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  r[0] = v.x;
+  r[1] = v.y;
+  r[2] = v.z;
+  r[3] = v.w;
+}
+
+template <int ACT, bool GATED>
+struct EpilogueVariant {
+  static constexpr int kAct = ACT;
+  static constexpr bool kGated = GATED;
+};
+
+template <int SHIFT, bool WIDE>
+struct ScaleVariant {
+  static constexpr int kShift = SHIFT;
+  static constexpr bool kWide = WIDE;
+};
+
+// One lane's share of a stage's scale columns: the weight's tiles as they are, the tokens' shifted by SHIFT words (-1:
+// the tile starts a band) plus one in the lanes with `carry`.  kWide: more than 128 tokens, two bands' words.
+template <int KIND, int CG, int SHIFT, bool kWide>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, const uint8_t* sf, int w_line, int line, bool carry) {
+  using C = FCfg<KIND, CG>;
+  constexpr int kWords = kWide ? 8 : 4;
+  constexpr int kBands = SHIFT < 0 ? (kWide ? 2 : 1) : (kWide ? 3 : 2);
+  constexpr int kStep = C::ATOMS > 1 ? 2 : 1;  // K-group tiles whose loads are in flight at once
+  uint32_t w[C::SFW_COLS];
+#pragma unroll
+  for (int a = 0; a < C::ATOMS; ++a) lds16(w + 4 * a, sf + 512 * a + w_line * 16);
+  const uint8_t* sfx = sf + C::BAND_BYTES + line * 16;
+#pragma unroll
+  for (int a0 = 0; a0 < C::ATOMS; a0 += kStep) {
+    uint32_t b[kStep][4 * kBands], x[kStep][kWords];
+#pragma unroll
+    for (int a = 0; a < kStep; ++a)
+#pragma unroll
+      for (int i = 0; i < kBands; ++i) lds16(b[a] + 4 * i, sfx + C::BAND_BYTES * i + 512 * (a0 + a));
+    if (a0 == 0) {
+      if constexpr (C::SFW_COLS == 16)
+        tmem_st_16cols(taddr, w);
+      else
+        tmem_st_4cols(taddr, w);
+    }
+#pragma unroll
+    for (int a = 0; a < kStep; ++a) {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        if constexpr (SHIFT < 0) x[a][j] = b[a][j];
+        else x[a][j] = carry ? b[a][SHIFT + j + 1] : b[a][SHIFT + j];
+      }
+    }
+    const uint32_t tx = taddr + C::SFW_COLS + C::X_WORDS * a0;
+    if constexpr (kStep * kWords == 16) {
+      tmem_st_16cols(tx, x[0]);
+    } else if constexpr (C::X_WORDS == kWords && kStep * kWords == 8) {
+      tmem_st_8cols(tx, x[0]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < kStep; ++a) tmem_st_4cols(tx + C::X_WORDS * a, x[a]);
+    }
+  }
+}
+
+// kF32: D in fp32, else bf16.  kRes: with a residual.  (Template parameters: with the accumulator in registers, the
+// epilogue has none to spare for what both sides of a branch would share.)
+template <int KIND, int CG, bool kF32, bool kRes>
 __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
-    fused_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                      const __grid_constant__ CUtensorMap tmXfull, const __grid_constant__ CUtensorMap tmSFW,
-                      const __grid_constant__ CUtensorMap tmSFX, const FusedParams p) {
+    fused_gemm_kernel(const __grid_constant__ FusedMaps maps, const FusedParams p) {
   using C = FCfg<KIND, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
-  uint8_t* table_mem = staging + C::EPI_WARPS * C::STG_BYTES;
+  uint8_t* table_mem = staging + C::EPI_WARPS * (2 * C::STG_BYTES + C::SCALE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(table_mem + C::TABLE_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* sf_ready = empty + C::STAGES;
@@ -236,11 +308,11 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_barrier_init();
-    prefetch_tensormap(&tmW);
-    prefetch_tensormap(&tmX);
-    prefetch_tensormap(&tmXfull);
-    prefetch_tensormap(&tmSFW);
-    prefetch_tensormap(&tmSFX);
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.sfw);
+    for (int i = 0; i < C::X_MAPS; ++i) prefetch_tensormap(&maps.x[i]);
+    for (int i = 0; i < C::X_BANDS; ++i) prefetch_tensormap(&maps.sfx[i]);
+    prefetch_tensormap(&maps.d);
   }
   if (warp == 1) {
     if constexpr (C::CG == 2) {
@@ -282,28 +354,26 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
           const int band = q.nb * C::CG + static_cast<int>(rank);  // of 128 weight rows
           const int x_rows = q.nmma / C::CG;
           const int x_row = q.row0 + static_cast<int>(rank) * x_rows;
-          const int boxes = (x_rows + C::X_BOX - 1) / C::X_BOX;
-          const int x_band = q.row0 >> 7;
+          const int x_box = (x_rows + 31) >> 5;
           const int x_bands = ((q.row0 & 127) + q.nmma + 127) >> 7;
-          const uint32_t tx = static_cast<uint32_t>(C::W_BYTES + boxes * C::X_BOX * 128 + C::BAND_BYTES * (1 + x_bands));
+          const CUtensorMap* mx = &maps.x[x_box - 1];
+          const CUtensorMap* msfx = &maps.sfx[x_bands - 1];
+          const uint32_t tx = static_cast<uint32_t>(C::W_BYTES + x_box * 4096 + C::BAND_BYTES * (1 + x_bands));
           for (int kb = 0; kb < p.num_kb; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
             uint8_t* st = smem + stage * C::STAGE_BYTES;
-            mbar_arrive_expect_tx(&full[stage], tx);
-            tma_load_3d(st, &tmW, &full[stage], kb * 128, band * 128, q.e);
-            if (boxes == C::X_ROWS / C::X_BOX) {
-              tma_load_2d(st + C::W_BYTES, &tmXfull, &full[stage], kb * 128, x_row);
-            } else {
-              for (int b = 0; b < boxes; ++b)
-                tma_load_2d(st + C::W_BYTES + b * C::X_BOX * 128, &tmX, &full[stage], kb * 128, x_row + b * C::X_BOX);
-            }
             uint8_t* sf = st + C::W_BYTES + C::X_BYTES;
-            tma_load_4d(sf, &tmSFW, &full[stage], 0, kb * C::ATOMS, band, q.e);
-            for (int b = 0; b < x_bands; ++b)
-              tma_load_3d(sf + C::BAND_BYTES * (1 + b), &tmSFX, &full[stage], 0, kb * C::ATOMS, x_band + b);
+            mbar_arrive_expect_tx(&full[stage], tx);
+            if (p.gated)
+              tma_load_5d(st, &maps.w, &full[stage], kb * 128, 0, 0, band * 8, q.e);
+            else
+              tma_load_3d(st, &maps.w, &full[stage], kb * 128, band * 128, q.e);
+            tma_load_2d(st + C::W_BYTES, mx, &full[stage], kb * 128, x_row);
+            tma_load_4d(sf, &maps.sfw, &full[stage], 0, kb * C::ATOMS, band, q.e);
+            tma_load_3d(sf + C::BAND_BYTES, msfx, &full[stage], 0, kb * C::ATOMS, q.row0 >> 7);
             ++issued[stage];
             if (++stage == C::STAGES) {
               stage = 0;
@@ -437,77 +507,52 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     uint64_t* sf_mine = leader ? sf_ready : sf_local;
+    // gated: the accumulator's rows are the weight's in the order of the epilogue (gated_row)
+    const int w_line = p.gated ? gated_row(static_cast<int>(lane)) : static_cast<int>(lane);
     for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
       const Tile q = table.get<C::TN, C::N_STEP>(t, p);
       // Scale row i of the tile is row (row0 & 127) + i of the loaded bands.  Line `lane` of tensor memory takes the
       // words of rows lane + 32 j, which all sit in line (row0 + lane) & 31 of the tiles, at word `shift` + j (plus
       // one in the lanes where row0 + lane carries into the next 32 rows) of the bands' words one after another.
-      const int shift = (q.row0 & 127) >> 5;
       const bool carry = (q.row0 & 31) + static_cast<int>(lane) >= 32;
       const int line = (q.row0 + static_cast<int>(lane)) & 31;
-      for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!mbar_wait(&full[stage], phase, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint8_t* sfw_s = smem + stage * C::STAGE_BYTES + C::W_BYTES + C::X_BYTES;
-        const uint8_t* sfx_s = sfw_s + C::BAND_BYTES;
-        const uint32_t taddr = tmem + lane_base + C::ACC_COLS + stage * C::SF_COLS;
-        uint32_t w[C::SFW_COLS];
-#pragma unroll
-        for (int a = 0; a < C::ATOMS; ++a) {
-          const uint4 v = *reinterpret_cast<const uint4*>(sfw_s + 512 * a + lane * 16);
-          w[4 * a + 0] = v.x;
-          w[4 * a + 1] = v.y;
-          w[4 * a + 2] = v.z;
-          w[4 * a + 3] = v.w;
-        }
-        if constexpr (C::SFW_COLS == 16)
-          tmem_st_16cols(taddr, w);
-        else
-          tmem_st_4cols(taddr, w);
-#pragma unroll
-        for (int a = 0; a < C::ATOMS; ++a) {
-          uint32_t b[4 * C::X_BANDS], x[C::X_WORDS];
-#pragma unroll
-          for (int i = 0; i < C::X_BANDS; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sfx_s + C::BAND_BYTES * i + 512 * a + line * 16);
-            b[4 * i + 0] = v.x;
-            b[4 * i + 1] = v.y;
-            b[4 * i + 2] = v.z;
-            b[4 * i + 3] = v.w;
+      // one loop over K for each variant: a choice inside it costs 3% of a large GEMM
+      auto stages = [&](auto variant) {
+        constexpr int kShift = decltype(variant)::kShift;
+        constexpr bool kWide = decltype(variant)::kWide;
+        for (int kb = 0; kb < p.num_kb; ++kb) {
+          if (!mbar_wait(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
           }
-          switch (shift) {
-            case 0:
-#pragma unroll
-              for (int j = 0; j < C::X_WORDS; ++j) x[j] = carry ? b[j + 1] : b[j];
-              break;
-            case 1:
-#pragma unroll
-              for (int j = 0; j < C::X_WORDS; ++j) x[j] = carry ? b[j + 2] : b[j + 1];
-              break;
-            case 2:
-#pragma unroll
-              for (int j = 0; j < C::X_WORDS; ++j) x[j] = carry ? b[j + 3] : b[j + 2];
-              break;
-            default:
-#pragma unroll
-              for (int j = 0; j < C::X_WORDS; ++j) x[j] = carry ? b[j + 4] : b[j + 3];
-              break;
+          copy_scales<KIND, CG, kShift, kWide>(tmem + lane_base + C::ACC_COLS + stage * C::SF_COLS,
+                                               smem + stage * C::STAGE_BYTES + C::W_BYTES + C::X_BYTES, w_line, line,
+                                               carry);
+          tmem_st_wait();
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sf_mine[stage]);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
-          if constexpr (C::X_WORDS == 8)
-            tmem_st_8cols(taddr + C::SFW_COLS + 8 * a, x);
-          else
-            tmem_st_4cols(taddr + C::SFW_COLS + 4 * a, x);
         }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_mine[stage]);
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
+      };
+      const int shift = (q.row0 & 127) == 0 ? -1 : (q.row0 & 127) >> 5;
+      if (CG == 2 && q.nmma > 128) {
+        if constexpr (CG == 2) {
+          if (shift < 0) stages(ScaleVariant<-1, true>{});
+          else if (shift == 0) stages(ScaleVariant<0, true>{});
+          else if (shift == 1) stages(ScaleVariant<1, true>{});
+          else if (shift == 2) stages(ScaleVariant<2, true>{});
+          else stages(ScaleVariant<3, true>{});
         }
+      } else {
+        if (shift < 0) stages(ScaleVariant<-1, false>{});
+        else if (shift == 0) stages(ScaleVariant<0, false>{});
+        else if (shift == 1) stages(ScaleVariant<1, false>{});
+        else if (shift == 2) stages(ScaleVariant<2, false>{});
+        else stages(ScaleVariant<3, false>{});
       }
     }
     if (!ok) {
@@ -516,36 +561,46 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // A lane of tensor memory is a weight row, a column a token.  A warp reads its 32 rows x up to 16 CHUNKS tokens
-    // into registers, hands the accumulator back, and turns them over through shared memory 16 tokens at a time:
-    // then lane (token, segment) holds 8 consecutive columns of one token's row of D, which are finished in fp32 and
-    // written with one 16-byte store (bf16), 64 bytes of a row per four lanes.
+    // A lane of tensor memory is a weight row, a column a token.  A warp reads its 32 rows x up to 16 STEPS tokens
+    // into registers as 8 x 8 fragments (thread t: row t / 4, tokens 2 (t % 4) and the next), hands the accumulator
+    // back, finishes the values in fp32, rounds them once and turns them over on the way to shared memory (stmatrix
+    // with a transpose), 16 tokens x 32 columns of D at a time, from where they go out as one TMA store.  (16-byte
+    // stores from the lanes took 25% longer over the whole GEMM; turning fp32 values over through shared memory and
+    // storing 8 tokens at a time took twice as long as the MMAs at K = 1536.)  The box that holds an expert's last
+    // rows is stored by the lanes, row by row: the rows after them belong to another expert.
     if constexpr (C::CG == 2) regs_inc<C::EPI_REGS>();
     const int ew = warp - C::FIRST_EPI_WARP;
     const int quarter = warp & 3;
     const int half = ew >> 2;
-    float* stg = reinterpret_cast<float*>(staging + ew * C::STG_BYTES);
-    const int seg = static_cast<int>(lane) & 3, sub = static_cast<int>(lane) >> 2;
+    const int fr = static_cast<int>(lane) >> 2, fc = 2 * (static_cast<int>(lane) & 3);  // fragment row, first token
     uint64_t* acc_mine = leader ? acc_empty : acc_local;
+    const uint64_t evict_first = l2_policy_evict_first();
+    float* scales = reinterpret_cast<float*>(staging + C::EPI_WARPS * 2 * C::STG_BYTES) + ew * 16 * C::STEPS;
+    uint32_t seq = 0;  // boxes of this warp (picks the staging buffer)
     int it = 0;
     for (int t = first_tile; t < num_tiles; t += tile_step, ++it) {
       const Tile q = table.get<C::TN, C::N_STEP>(t, p);
       const int buf = it % C::ACC_BUFS;
       const int width = C::CG == 2 ? q.nmma / 2 : q.nmma;  // tokens per epilogue warp
       const int tok0 = half * width;                       // this warp's first token of the tile
-      const int n0 = (q.nb * C::CG + static_cast<int>(rank)) * 128 + quarter * 32 + seg * 8;
-      const bool n_ok = n0 < p.N;
+      const int col0 = (q.nb * C::CG + static_cast<int>(rank)) * 128 + quarter * 32;  // first weight row
       const float alpha = p.alpha != nullptr ? __ldg(p.alpha + q.e) : 1.0f;
-      uint4 bias = make_uint4(0u, 0u, 0u, 0u);  // of this lane's 8 columns
-      if (p.bias != nullptr && n_ok)
-        bias = __ldg(reinterpret_cast<const uint4*>(p.bias + static_cast<int64_t>(q.e) * p.N + n0));
-      // alpha x row scale of this warp's tokens, one per lane, handed out by shuffles
-      float scale[(C::CHUNKS + 1) / 2];
+      float bias[4];  // of fragment rows fr + 8 i
 #pragma unroll
-      for (int j = 0; j < (C::CHUNKS + 1) / 2; ++j) {
-        const int tk = tok0 + 32 * j + static_cast<int>(lane);
-        scale[j] = (p.row_scale != nullptr && tk < q.cnt) ? __fmul_rn(alpha, __ldg(p.row_scale + q.row0 + tk)) : alpha;
+      for (int i = 0; i < 4; ++i) {
+        const int n = col0 + (p.gated ? gated_row(fr + 8 * i) : fr + 8 * i);
+        bias[i] = p.bias != nullptr && n < p.N ? bf16_bits_to_f32(__ldg(p.bias + static_cast<int64_t>(q.e) * p.N + n))
+                                               : 0.0f;
       }
+      // alpha x row scale of this warp's tokens
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 16 * C::STEPS; j += 32) {
+        const int tk = tok0 + j + static_cast<int>(lane);
+        scales[j + lane] =
+            (p.row_scale != nullptr && tk < q.cnt) ? __fmul_rn(alpha, __ldg(p.row_scale + q.row0 + tk)) : alpha;
+      }
+      __syncwarp();
       const uint32_t par = static_cast<uint32_t>(it / C::ACC_BUFS) & 1u;
       const bool got = C::CG == 2 ? mbar_wait_cluster(&acc_full[buf], par, abort_flag)
                                   : mbar_wait(&acc_full[buf], par, abort_flag);
@@ -557,96 +612,180 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
       tc_fence_after_sync();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                              static_cast<uint32_t>(buf * C::TN + tok0);
-      uint32_t r[C::CHUNKS][16];  // columns past `width` are read too, within the accumulator, and not used
+      // columns past `width` are read too, within the accumulator, and not used
+      uint32_t r[2][C::STEPS / 4][32];  // [row half][64 tokens][4 x octet + 2 x row block + token]
 #pragma unroll
-      for (int c = 0; c < C::CHUNKS; ++c) tmem_ld_16cols(taddr + 16u * c, r[c]);
+      for (int c = 0; c < C::STEPS / 4; ++c) {
+        tmem_ld_frag_64cols(taddr + 64u * c, r[0][c]);
+        tmem_ld_frag_64cols(taddr + (16u << 16) + 64u * c, r[1][c]);
+      }
       tmem_ld_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(C::CG == 2 ? acc_mine : &acc_empty[buf]);
 
-#pragma unroll
-      for (int c = 0; c < C::CHUNKS; ++c) {
-        if (16 * c < width && tok0 + 16 * c < q.cnt) {  // warp-uniform
+      // One straight line of code per activation and gate: the unrolled steps (the accumulator is in registers, so
+      // they cannot be a loop) would otherwise carry every branch.
+      auto finish = [&](auto kind) {
+        constexpr int kAct = decltype(kind)::kAct;
+        constexpr bool kGated = decltype(kind)::kGated;
+        constexpr int kCols = kGated ? 16 : 32;  // columns of D per warp
+        const int cols = kGated ? p.N >> 1 : p.N;
+        const int d_col0 = kGated ? col0 >> 1 : col0;
+
+        // A box of D in a staging buffer: rows of kRow bytes, 16-byte chunks swizzled as the TMA store reads them.
+        auto chunk = [](int row, int c, int row_bytes) {
+          return row * row_bytes + 16 * (c ^ (row_bytes == 128 ? row & 7 : row_bytes == 64 ? (row >> 1) & 3 : (row >> 2) & 1));
+        };
+        auto open_box = [&]() {
+          if (lane == 0) bulk_wait_read_allow<1>();  // the store from this buffer, two boxes back, has read it
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) stg[i * C::STG_LD + lane] = __uint_as_float(r[c][i]);
-          __syncwarp();
+          return staging + (ew * 2 + (seq++ & 1)) * C::STG_BYTES;
+        };
+        // the residual's box, one 16-byte chunk per lane and turn, into the buffer
+        auto fill_box = [&](uint8_t* box, int tb, int rows, int row_bytes, int esize) {
+          const int per_row = row_bytes >> 4;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const int i = 8 * h + sub;  // token of the chunk
-            const float sc = __shfl_sync(0xFFFFFFFFu, scale[c / 2], (16 * c + i) & 31);
-            const int tk = tok0 + 16 * c + i;
-            const int64_t m = q.row0 + tk;
-            const float4 lo4 = *reinterpret_cast<const float4*>(stg + i * C::STG_LD + 8 * seg);
-            const float4 hi4 = *reinterpret_cast<const float4*>(stg + i * C::STG_LD + 8 * seg + 4);
-            float y[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
-            const uint32_t bw[4] = {bias.x, bias.y, bias.z, bias.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = __fmaf_rn(y[2 * j], sc, bf16_bits_to_f32(bw[j] & 0xFFFFu));
-              y[2 * j + 1] = __fmaf_rn(y[2 * j + 1], sc, bf16_bits_to_f32(bw[j] >> 16));
+          for (int c = static_cast<int>(lane); c < rows * per_row; c += 32) {
+            const int row = c / per_row, cc = c - row * per_row;
+            const int col = d_col0 + cc * (16 / esize);
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (tb + row < q.cnt && col < cols)
+              v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) +
+                                                  ((q.row0 + tb + row) * p.ld_res + col) * esize);
+            *reinterpret_cast<uint4*>(box + chunk(row, cc, row_bytes)) = v;
+          }
+          __syncwarp();
+        };
+        auto close_box = [&](uint8_t* box, int tb, int rows, int row_bytes, int esize) {
+          if (tb + rows <= q.cnt) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && d_col0 < cols) tma_store_2d_hint(&maps.d, box, d_col0, q.row0 + tb, evict_first);
+          } else {
+            __syncwarp();
+            const int per_row = row_bytes >> 4;
+#pragma unroll 1
+            for (int c = static_cast<int>(lane); c < rows * per_row; c += 32) {
+              const int row = c / per_row, cc = c - row * per_row;
+              const int col = d_col0 + cc * (16 / esize);
+              if (tb + row < q.cnt && col < cols)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.D) + ((q.row0 + tb + row) * p.ld_d + col) * esize) =
+                    *reinterpret_cast<const uint4*>(box + chunk(row, cc, row_bytes));
             }
-            const bool store = n_ok && tk < q.cnt;
-            if (!p.gated) {
-              activate<8, 1>(y, p.act);
-              if (store) {
-                if (p.out_f32) {
-                  if (p.residual != nullptr) {
-                    const float4* rp =
-                        reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + m * p.ld_res + n0);
-                    const float4 u = rp[0], v = rp[1];
-                    y[0] += u.x, y[1] += u.y, y[2] += u.z, y[3] += u.w;
-                    y[4] += v.x, y[5] += v.y, y[6] += v.z, y[7] += v.w;
-                  }
-                  float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.D) + m * p.ld_d + n0);
-                  __stcs(d, make_float4(y[0], y[1], y[2], y[3]));
-                  __stcs(d + 1, make_float4(y[4], y[5], y[6], y[7]));
-                } else {
-                  if (p.residual != nullptr) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.residual) +
-                                                                    m * p.ld_res + n0);
-                    const uint32_t rw[4] = {v.x, v.y, v.z, v.w};
+          }
+          if (lane == 0) bulk_commit_group();  // one group per box, empty or not: open_box counts boxes
+        };
+
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                      y[2 * j] += bf16_bits_to_f32(rw[j] & 0xFFFFu);
-                      y[2 * j + 1] += bf16_bits_to_f32(rw[j] >> 16);
-                    }
-                  }
-                  __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.D) + m * p.ld_d + n0),
-                         make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                    pack_bf16x2(y[6], y[7])));
-                }
+        for (int s = 0; s < C::STEPS; ++s) {
+          const int tb = tok0 + 16 * s;  // first token of the step
+          if (16 * s < width && tb < q.cnt) {  // warp-uniform
+            // z[o][n][u]: octet of tokens o, 8-column block n, token fc + u
+            constexpr int kBlocks = kGated ? 2 : 4;
+            float z[2][kBlocks][2];
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const float2 sc2 = *reinterpret_cast<const float2*>(scales + 16 * s + 8 * o + fc);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float sc = u == 0 ? sc2.x : sc2.y;
+                const int at = 4 * ((2 * s + o) & 7) + u;
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  y[i] = __fmaf_rn(__uint_as_float(r[i >> 1][s / 4][at + 2 * (i & 1)]), sc, bias[i]);
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i)
+                  z[o][i][u] = kGated ? activate<kAct>(y[2 * i & 3]) * y[(2 * i + 1) & 3] : activate<kAct>(y[i]);
               }
-            } else {
-              activate<8, 2>(y, p.act);
-              float z[4] = {y[0] * y[1], y[2] * y[3], y[4] * y[5], y[6] * y[7]};
-              const int nh = n0 >> 1;
-              if (store) {
-                if (p.out_f32) {
-                  if (p.residual != nullptr) {
-                    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) +
-                                                                      m * p.ld_res + nh);
-                    z[0] += u.x, z[1] += u.y, z[2] += u.z, z[3] += u.w;
-                  }
-                  __stcs(reinterpret_cast<float4*>(static_cast<float*>(p.D) + m * p.ld_d + nh),
-                         make_float4(z[0], z[1], z[2], z[3]));
+            }
+            if constexpr (!kF32) {
+              constexpr int kRow = 2 * kCols;
+              uint8_t* box = open_box();
+              // lane l addresses row l % 8 of matrix l / 8 of a group of four
+              const int m = static_cast<int>(lane) >> 3;
+              uint32_t at[kGated ? 1 : 2];
+              if constexpr (kGated) {
+                at[0] = smem_u32(box) + chunk(8 * (m >> 1) + (lane & 7), m & 1, kRow);  // (octet, block)
+              } else {
+                at[0] = smem_u32(box) + chunk(lane & 7, m, kRow);
+                at[1] = smem_u32(box) + chunk(8 + (lane & 7), m, kRow);
+              }
+              uint32_t w[2][kBlocks];
+              if constexpr (kRes) {
+                fill_box(box, tb, 16, kRow, 2);
+                if constexpr (kGated) {
+                  ldmatrix_x4_trans(at[0], w[0][0], w[0][1], w[1][0], w[1][1]);
                 } else {
-                  if (p.residual != nullptr) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.residual) +
-                                                                    m * p.ld_res + nh);
-                    z[0] += bf16_bits_to_f32(v.x & 0xFFFFu), z[1] += bf16_bits_to_f32(v.x >> 16);
-                    z[2] += bf16_bits_to_f32(v.y & 0xFFFFu), z[3] += bf16_bits_to_f32(v.y >> 16);
+                  ldmatrix_x4_trans(at[0], w[0][0], w[0][1], w[0][2 % kBlocks], w[0][3 % kBlocks]);
+                  ldmatrix_x4_trans(at[1], w[1][0], w[1][1], w[1][2 % kBlocks], w[1][3 % kBlocks]);
+                }
+                __syncwarp();  // every lane has read before the result takes the residual's place
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                  for (int i = 0; i < kBlocks; ++i) {
+                    z[o][i][0] += bf16_bits_to_f32(w[o][i] & 0xFFFFu);
+                    z[o][i][1] += bf16_bits_to_f32(w[o][i] >> 16);
                   }
-                  __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.D) + m * p.ld_d + nh),
-                         make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3])));
+              }
+#pragma unroll
+              for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) w[o][i] = pack_bf16x2(z[o][i][0], z[o][i][1]);
+              if constexpr (kGated) {
+                stmatrix_x4_trans(at[0], w[0][0], w[0][1], w[1][0], w[1][1]);
+              } else {
+                stmatrix_x4_trans(at[0], w[0][0], w[0][1], w[0][2 % kBlocks], w[0][3 % kBlocks]);
+                stmatrix_x4_trans(at[1], w[1][0], w[1][1], w[1][2 % kBlocks], w[1][3 % kBlocks]);
+              }
+              close_box(box, tb, 16, kRow, 2);
+            } else {
+              constexpr int kRow = 4 * kCols;
+              constexpr int kRows = kGated ? 16 : 8;  // a box is 1 KB
+#pragma unroll
+              for (int o0 = 0; o0 < 2; o0 += kRows / 8) {
+                if (tb + 8 * o0 < q.cnt) {  // warp-uniform
+                  uint8_t* box = open_box();
+                  if constexpr (kRes) fill_box(box, tb + 8 * o0, kRows, kRow, 4);
+#pragma unroll
+                  for (int o = o0; o < o0 + kRows / 8; ++o)
+#pragma unroll
+                    for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                      for (int u = 0; u < 2; ++u) {
+                        const int row = 8 * (o - o0) + fc + u, n = 8 * i + fr;
+                        float* at = reinterpret_cast<float*>(box + chunk(row, n >> 2, kRow)) + (n & 3);
+                        *at = kRes ? z[o][i][u] + *at : z[o][i][u];
+                      }
+                  close_box(box, tb + 8 * o0, kRows, kRow, 4);
                 }
               }
             }
           }
         }
+      };
+      if (p.gated) {
+        switch (p.act) {
+          case BSP_ACT_RELU: finish(EpilogueVariant<BSP_ACT_RELU, true>{}); break;
+          case BSP_ACT_GELU: finish(EpilogueVariant<BSP_ACT_GELU, true>{}); break;
+          case BSP_ACT_GELU_TANH: finish(EpilogueVariant<BSP_ACT_GELU_TANH, true>{}); break;
+          case BSP_ACT_SILU: finish(EpilogueVariant<BSP_ACT_SILU, true>{}); break;
+          default: finish(EpilogueVariant<BSP_ACT_NONE, true>{}); break;
+        }
+      } else {
+        switch (p.act) {
+          case BSP_ACT_RELU: finish(EpilogueVariant<BSP_ACT_RELU, false>{}); break;
+          case BSP_ACT_GELU: finish(EpilogueVariant<BSP_ACT_GELU, false>{}); break;
+          case BSP_ACT_GELU_TANH: finish(EpilogueVariant<BSP_ACT_GELU_TANH, false>{}); break;
+          case BSP_ACT_SILU: finish(EpilogueVariant<BSP_ACT_SILU, false>{}); break;
+          default: finish(EpilogueVariant<BSP_ACT_NONE, false>{}); break;
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before_sync();
@@ -670,24 +809,31 @@ struct FusedArgs {
   int64_t row_bytes, tiles_per_band;
 };
 
-template <int KIND, int CG>
-int launch_fused(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cudaStream_t stream) {
+template <int KIND, int CG, bool kF32, bool kRes>
+int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cudaStream_t stream) {
   using C = FCfg<KIND, CG>;
-  auto kernel = fused_gemm_kernel<KIND, CG>;
+  auto kernel = fused_gemm_kernel<KIND, CG, kF32, kRes>;
   static bool attr_set[64] = {};
   if (!attr_set[dev.id]) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
       return launch_status();
     attr_set[dev.id] = true;
   }
-  CUtensorMap tmW, tmX, tmXfull, tmSFW, tmSFX;
+  FusedMaps maps;
   int st;
-  if ((st = encode_experts(&tmW, a.B, p.E, p.N, a.row_bytes, 128)) != BSP_OK) return st;
-  if ((st = encode_operand(&tmX, a.A, p.M, a.row_bytes, C::X_BOX)) != BSP_OK) return st;
-  if ((st = encode_operand(&tmXfull, a.A, p.M, a.row_bytes, C::X_ROWS)) != BSP_OK) return st;
-  if ((st = encode_expert_scales(&tmSFW, a.sfB, p.E, ceil_div(p.N, 128), a.tiles_per_band, C::ATOMS)) != BSP_OK)
+  if ((st = p.gated ? encode_experts_gated(&maps.w, a.B, p.E, p.N, a.row_bytes)
+                    : encode_experts(&maps.w, a.B, p.E, p.N, a.row_bytes, 128)) != BSP_OK)
     return st;
-  if ((st = encode_scales(&tmSFX, a.sfA, ceil_div(p.M, 128), a.tiles_per_band, C::ATOMS, 1)) != BSP_OK) return st;
+  if ((st = encode_expert_scales(&maps.sfw, a.sfB, p.E, ceil_div(p.N, 128), a.tiles_per_band, C::ATOMS)) != BSP_OK)
+    return st;
+  for (int i = 0; i < C::X_MAPS; ++i)
+    if ((st = encode_operand(&maps.x[i], a.A, p.M, a.row_bytes, 32 * (i + 1))) != BSP_OK) return st;
+  for (int i = 0; i < C::X_BANDS; ++i)
+    if ((st = encode_scales(&maps.sfx[i], a.sfA, ceil_div(p.M, 128), a.tiles_per_band, C::ATOMS, i + 1)) != BSP_OK)
+      return st;
+  if ((st = encode_rows(&maps.d, p.D, p.M, p.gated ? p.N / 2 : p.N, p.ld_d, kF32, kF32 && !p.gated ? 8 : 16,
+                        p.gated ? 16 : 32)) != BSP_OK)
+    return st;
 
   p.num_kb = static_cast<int>(ceil_div(a.row_bytes, 128));
   p.panels = static_cast<int>(ceil_div(p.N, 128 * CG));
@@ -728,8 +874,17 @@ int launch_fused(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cudaS
                                      : (24ll << 20) / (static_cast<int64_t>(C::TN) * a.row_bytes * 17 / 16);
   p.group_m = static_cast<int>(g < 8 ? 8 : g > (1 << 20) ? (1 << 20) : g);
   cfg.gridDim = dim3(static_cast<unsigned>(groups * CG), 1, 1);
-  if (cudaLaunchKernelEx(&cfg, kernel, tmW, tmX, tmXfull, tmSFW, tmSFX, p) != cudaSuccess) return launch_status();
+  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) return launch_status();
   return launch_status();
+}
+
+template <int KIND, int CG>
+int launch_fused(const DeviceInfo& dev, const FusedArgs& a, const FusedParams& p, bool f32, cudaStream_t stream) {
+  if (f32)
+    return p.residual ? launch_variant<KIND, CG, true, true>(dev, a, p, stream)
+                      : launch_variant<KIND, CG, true, false>(dev, a, p, stream);
+  return p.residual ? launch_variant<KIND, CG, false, true>(dev, a, p, stream)
+                    : launch_variant<KIND, CG, false, false>(dev, a, p, stream);
 }
 
 template <int KIND>
@@ -768,7 +923,6 @@ int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
   p.E = static_cast<int>(E);
   p.act = act;
   p.gated = gated;
-  p.out_f32 = d_dtype == BSP_OUT_F32;
   p.offsets = offsets;
   p.alpha = alpha;
   p.row_scale = row_scale;
@@ -779,8 +933,8 @@ int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
   p.ld_d = ld_d;
   p.err = dev.err_word;
   // CTA pairs for experts of more than 64 rows on average
-  if (ceil_div(M, E) > 64) return launch_fused<KIND, 2>(dev, a, p, stream);
-  return launch_fused<KIND, 1>(dev, a, p, stream);
+  if (ceil_div(M, E) > 64) return launch_fused<KIND, 2>(dev, a, p, d_dtype == BSP_OUT_F32, stream);
+  return launch_fused<KIND, 1>(dev, a, p, d_dtype == BSP_OUT_F32, stream);
 }
 
 }  // namespace
