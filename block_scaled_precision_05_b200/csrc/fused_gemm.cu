@@ -74,8 +74,9 @@ struct FCfg {
   static constexpr int FIRST_SF_WARP = 4, FIRST_EPI_WARP = 8;
   static constexpr int THREADS = (8 + EPI_WARPS) * 32;
   static constexpr int STEPS = TN / (EPI_WARPS / 4) / 16;  // steps of 16 tokens per epilogue warp
-  // CTA pairs: warpgroups 0 and 1 hand registers to the epilogue, which holds 128 accumulator columns a thread
-  static constexpr int WG0_REGS = 40, SF_REGS = 88, EPI_REGS = 192;
+  // CTA pairs: warpgroups 0 and 1 hand registers to the epilogue, which holds 128 accumulator columns a thread.  (With
+  // 40 for the first, as in gemm.cu, its loops spill: 7% of a large GEMM.)
+  static constexpr int WG0_REGS = 72, SF_REGS = 88, EPI_REGS = 176;
   static_assert(CG == 1 || 128 * (WG0_REGS + SF_REGS + 2 * EPI_REGS) == THREADS * (65536 / THREADS), "register split");
   static constexpr int STG_BYTES = 1024;  // staging: two buffers per warp, each a box of D for one TMA store
   static constexpr int SCALE_BYTES = 16 * STEPS * 4;  // and its tokens' scales
@@ -346,8 +347,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         uint32_t stage = 0, phase = 0;
-        uint32_t issued[C::STAGES];
-        for (int s = 0; s < C::STAGES; ++s) issued[s] = 0;
+        uint32_t total = 0;  // stages issued
         bool ok = true;
         for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
           const Tile q = table.get<C::TN, C::N_STEP>(t, p);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             tma_load_2d(st + C::W_BYTES, mx, &full[stage], kb * 128, x_row);
             tma_load_4d(sf, &maps.sfw, &full[stage], 0, kb * C::ATOMS, band, q.e);
             tma_load_3d(sf + C::BAND_BYTES, msfx, &full[stage], 0, kb * C::ATOMS, q.row0 >> 7);
-            ++issued[stage];
+            ++total;
             if (++stage == C::STAGES) {
               stage = 0;
               phase ^= 1u;
@@ -386,8 +386,9 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
           raise_error(p.err, kErrTimeout);
         }
         // Every issued copy must have landed before the CTA may exit.
-        for (int s = 0; s < C::STAGES; ++s)
-          if (issued[s] && !mbar_wait(&full[s], (issued[s] - 1u) & 1u, nullptr)) raise_error(p.err, kErrTimeout);
+        for (uint32_t s = 0; s < C::STAGES; ++s)
+          if (total > s && !mbar_wait(&full[s], ((total - 1u - s) / C::STAGES) & 1u, nullptr))
+            raise_error(p.err, kErrTimeout);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -626,6 +627,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
 
       // One straight line of code per activation and gate: the unrolled steps (the accumulator is in registers, so
       // they cannot be a loop) would otherwise carry every branch.
+      const int lim = min(width, q.cnt - tok0);
       auto finish = [&](auto kind) {
         constexpr int kAct = decltype(kind)::kAct;
         constexpr bool kGated = decltype(kind)::kGated;
@@ -680,7 +682,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
 #pragma unroll
         for (int s = 0; s < C::STEPS; ++s) {
           const int tb = tok0 + 16 * s;  // first token of the step
-          if (16 * s < width && tb < q.cnt) {  // warp-uniform
+          if (16 * s < lim) {  // warp-uniform
             // z[o][n][u]: octet of tokens o, 8-column block n, token fc + u
             constexpr int kBlocks = kGated ? 2 : 4;
             float z[2][kBlocks][2];
