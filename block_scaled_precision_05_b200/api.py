@@ -20,7 +20,6 @@ Sources (page title, then symbol):
 from __future__ import annotations
 
 import ctypes
-import math
 from dataclasses import dataclass
 
 import torch
@@ -28,8 +27,10 @@ import torch
 from . import _native as nat
 
 
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _stream(device: int | None = None) -> int:
+    """The current stream's handle, of the current device unless given.  The raw getter: a torch.cuda.Stream object
+    made for each launch takes 3 us."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if device is None else device)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -436,24 +437,27 @@ def _activation_code(activation: str | None) -> int:
 
 def _check_operand(what: str, codes: torch.Tensor, sf: torch.Tensor, shape: tuple, sf_bytes: int) -> None:
     """A hand-made operand whose buffers are smaller than its sizes say would be read out of range."""
-    if codes.dtype != torch.uint8 or tuple(codes.shape) != shape or not codes.is_contiguous():
+    if codes.dtype is not torch.uint8 or codes.shape != shape or not codes.is_contiguous():
         raise ValueError(f"{what}: expected contiguous uint8 codes of shape {shape}, got {tuple(codes.shape)}")
-    if sf.dtype != torch.uint8 or sf.numel() != sf_bytes or not sf.is_contiguous():
+    if sf.dtype is not torch.uint8 or sf.numel() != sf_bytes or not sf.is_contiguous():
         raise ValueError(f"{what}: expected {sf_bytes} contiguous scale bytes, got {sf.numel()}")
 
 
-def _check_vector(name: str, t: torch.Tensor | None, dtype: torch.dtype, shape: tuple) -> None:
-    if t is not None and (t.dtype != dtype or not t.is_contiguous() or t.numel() != math.prod(shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {math.prod(shape)} elements {shape}")
+def _check_vector(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int) -> None:
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
 
 
-def _one_device(first: torch.Tensor, *ts: torch.Tensor | None) -> torch.device:
-    """The operands' device; the launch goes to that device's current stream."""
-    _require_cuda(first, *ts)
+def _one_device(first: torch.Tensor, *ts: torch.Tensor | None) -> int:
+    """The operands' device, whose current stream the launch goes to."""
+    index = first.get_device()
     for t in ts:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
+            _require_cuda(first, *ts)
             raise ValueError(f"operands on different devices: {first.device} and {t.device}")
-    return first.device
+    if index < 0:
+        _require_cuda(first)
+    return index
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -468,37 +472,76 @@ def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
     return gap % ld < a.shape[1] or -gap % ld < a.shape[1]  # column ranges modulo the common row stride
 
 
-def _gemm_fused(fp4: bool, a, b, alpha, row_scale, bias, out_dtype, out, activation, gated, residual) -> torch.Tensor:
-    """nvfp4_gemm / mxfp8_gemm with an activation, a gate or a residual."""
-    act = _activation_code(activation)
-    acodes, bcodes = (a.codes, b.codes) if fp4 else (a.q, b.q)
-    M, N, K = a.rows, b.rows, a.K
+def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual):
+    """The GEMMs with a fused epilogue: dense (offsets None, b one weight) and grouped (b stacked).  One path for both,
+    kept short: the smallest calls take as long on the host as on the GPU."""
+    act = ACTIVATIONS.get(activation, -1)
+    if act < 0:
+        _activation_code(activation)
+    if fp4:
+        acodes, bcodes = a.codes, b.codes
+        if a.sf_layout != "128x4" or (offsets is None and b.sf_layout != "128x4"):
+            raise ValueError("a fused epilogue or a grouped GEMM needs scales in the 128x4 layout")
+    else:
+        acodes, bcodes = a.q, b.q
+    K = a.K
+    if K != b.K:
+        raise ValueError("A and B disagree on K")
+    M = acodes.shape[0]
+    width = K // 2 if fp4 else K
+    tiles = ((K // (16 if fp4 else 32) + 3) // 4) * 512  # scale bytes per 128 rows
+    if offsets is None:
+        E, N = 1, bcodes.shape[0]
+        shape = (N, width)
+    else:
+        E, N = bcodes.shape[0], bcodes.shape[1]
+        shape = (E, N, width)
+    index = _one_device(acodes, a.sf, bcodes, b.sf, offsets, alpha, row_scale, bias, residual, out)
+    _check_operand("A", acodes, a.sf, (M, width), (M + 127) // 128 * tiles)
+    _check_operand("B", bcodes, b.sf, shape, E * ((N + 127) // 128) * tiles)
+    if alpha is not None:
+        _check_vector("alpha", alpha, torch.float32, E)
+    if row_scale is not None:
+        _check_vector("row_scale", row_scale, torch.float32, M)
+    if bias is not None:
+        _check_vector("bias", bias, torch.bfloat16, E * N)
     if gated and N % 2 != 0:
         raise ValueError("a gated weight has an even number of rows")
-    dev = _one_device(acodes, a.sf, bcodes, b.sf, alpha, row_scale, bias, residual, out)
     cols = N // 2 if gated else N
-    out, d_dtype = _out(M, cols, out_dtype, dev, out)
+    if out is None and out_dtype in (torch.bfloat16, torch.float32):
+        out = torch.empty((M, cols), dtype=out_dtype, device=acodes.device)
+    else:
+        out, _ = _out(M, cols, out_dtype, acodes.device, out)
+    ld_res = 0
     if residual is not None:
-        if residual.dtype != out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
+        if residual.dtype is not out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
             raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
-        same = residual.data_ptr() == out.data_ptr() and residual.stride(0) == out.stride(0)
-        if not same and _overlap(residual, out):
+        ld_res = residual.stride(0)
+        if (residual.data_ptr() != out.data_ptr() or ld_res != out.stride(0)) and _overlap(residual, out):
             raise ValueError("residual may be the output itself, but must not overlap it otherwise")
-    _check_epilogue_args(alpha, row_scale, bias, N)
-    _check_vector("alpha", alpha, torch.float32, (1,))
-    _check_vector("row_scale", row_scale, torch.float32, (M,))
-    width, sf_bytes = (K // 2, nvfp4_sf_bytes) if fp4 else (K, mxfp8_sf_bytes)
-    _check_operand("A", acodes, a.sf, (M, width), sf_bytes(M, K))
-    _check_operand("B", bcodes, b.sf, (N, width), sf_bytes(N, K))
-    tail = [act, int(gated), _ptr(residual), residual.stride(0) if residual is not None else 0, _ptr(out), d_dtype,
-            out.stride(0)]
-    with torch.cuda.device(dev):
-        head = [_ptr(acodes), _ptr(a.sf), _ptr(bcodes), _ptr(b.sf), M, N, K, _ptr(alpha)]
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
+
+    L, d_dtype, ld, stream = nat.lib(), nat.BSP_OUT_F32 if out.dtype is torch.float32 else nat.BSP_OUT_BF16, \
+        out.stride(0), _stream(index)
+    pa, psa, pb, psb, pd = acodes.data_ptr(), a.sf.data_ptr(), bcodes.data_ptr(), b.sf.data_ptr(), out.data_ptr()
+    palpha, pbias, gated = _ptr(alpha), _ptr(bias), int(gated)
+    if offsets is None:
         if fp4:
-            st = nat.lib().nvfp4_gemm_fused(*head, _ptr(row_scale), _ptr(bias), *tail, _stream())
+            st = L.nvfp4_gemm_fused(pa, psa, pb, psb, M, N, K, palpha, _ptr(row_scale), pbias, act, gated,
+                                    _ptr(residual), ld_res, pd, d_dtype, ld, stream)
         else:
-            st = nat.lib().mxfp8_gemm_fused(*head, _ptr(bias), *tail, _stream())
-    nat.check(st, "nvfp4_gemm_fused" if fp4 else "mxfp8_gemm_fused")
+            st = L.mxfp8_gemm_fused(pa, psa, pb, psb, M, N, K, palpha, pbias, act, gated, _ptr(residual), ld_res, pd,
+                                    d_dtype, ld, stream)
+    elif fp4:
+        st = L.nvfp4_grouped_gemm(pa, psa, pb, psb, offsets.data_ptr(), E, M, N, K, palpha, _ptr(row_scale), pbias, act,
+                                  gated, pd, d_dtype, ld, stream)
+    else:
+        st = L.mxfp8_grouped_gemm(pa, psa, pb, psb, offsets.data_ptr(), E, M, N, K, palpha, pbias, act, gated, pd,
+                                  d_dtype, ld, stream)
+    if st:
+        nat.check(st, "fused GEMM" if offsets is None else "grouped GEMM")
     return out
 
 
@@ -518,9 +561,7 @@ def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, alpha: torch.Tensor | None = None
     if a.K != b.K:
         raise ValueError("A and B disagree on K")
     if activation is not None or gated or residual is not None:
-        if a.sf_layout != "128x4" or b.sf_layout != "128x4":
-            raise ValueError("an activation, a gate or a residual needs scales in the 128x4 layout")
-        return _gemm_fused(True, a, b, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
+        return _fused(True, a, b, None, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
     _require_cuda(a.codes, b.codes, alpha, row_scale, bias)
     M, N = a.rows, b.rows
     _check_epilogue_args(alpha, row_scale, bias, N)
@@ -543,7 +584,7 @@ def mxfp8_gemm(a: MXFP8Tensor, b: MXFP8Tensor, alpha: torch.Tensor | None = None
     if a.K != b.K:
         raise ValueError("A and B disagree on K")
     if activation is not None or gated or residual is not None:
-        return _gemm_fused(False, a, b, alpha, None, bias, out_dtype, out, activation, gated, residual)
+        return _fused(False, a, b, None, alpha, None, bias, out_dtype, out, activation, gated, residual)
     _require_cuda(a.q, b.q, alpha, bias)
     M, N = a.rows, b.rows
     _check_epilogue_args(alpha, None, bias, N)
@@ -629,34 +670,12 @@ def mxfp8_quantize_experts(w: torch.Tensor) -> MXFP8Experts:
 
 
 def _grouped_gemm(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated):
-    if a.K != b.K:
-        raise ValueError("A and B disagree on K")
-    act = _activation_code(activation)
-    acodes, bcodes = (a.codes, b.codes) if fp4 else (a.q, b.q)
-    M, E, N, K = a.rows, b.experts, b.rows, a.K
-    if E < 1 or E > nat.BSP_MAX_EXPERTS:
+    E = b.experts
+    if not 1 <= E <= nat.BSP_MAX_EXPERTS:
         raise ValueError(f"1 to {nat.BSP_MAX_EXPERTS} experts, got {E}")
-    if gated and N % 2 != 0:
-        raise ValueError("a gated weight has an even number of rows")
-    dev = _one_device(acodes, a.sf, bcodes, b.sf, offsets, alpha, row_scale, bias, out)
-    if offsets is None or offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,) or not offsets.is_contiguous():
+    if offsets is None or offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets must be a contiguous int32 tensor of {E + 1} elements")
-    width, sf_bytes = (K // 2, nvfp4_sf_bytes) if fp4 else (K, mxfp8_sf_bytes)
-    _check_operand("A", acodes, a.sf, (M, width), sf_bytes(M, K))
-    _check_operand("B", bcodes, b.sf, (E, N, width), E * sf_bytes(N, K))
-    _check_vector("alpha", alpha, torch.float32, (E,))
-    _check_vector("row_scale", row_scale, torch.float32, (M,))
-    _check_vector("bias", bias, torch.bfloat16, (E, N))
-    out, d_dtype = _out(M, N // 2 if gated else N, out_dtype, dev, out)
-    with torch.cuda.device(dev):
-        head = [_ptr(acodes), _ptr(a.sf), _ptr(bcodes), _ptr(b.sf), _ptr(offsets), E, M, N, K, _ptr(alpha)]
-        tail = [_ptr(bias), act, int(gated), _ptr(out), d_dtype, out.stride(0), _stream()]
-        if fp4:
-            st = nat.lib().nvfp4_grouped_gemm(*head, _ptr(row_scale), *tail)
-        else:
-            st = nat.lib().mxfp8_grouped_gemm(*head, *tail)
-    nat.check(st, "nvfp4_grouped_gemm" if fp4 else "mxfp8_grouped_gemm")
-    return out
+    return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, None)
 
 
 def nvfp4_grouped_gemm(a: NVFP4Tensor, b: NVFP4Experts, offsets: torch.Tensor, alpha: torch.Tensor | None = None,
@@ -672,8 +691,6 @@ def nvfp4_grouped_gemm(a: NVFP4Tensor, b: NVFP4Experts, offsets: torch.Tensor, a
     [M, K] activation; offsets int32 [E + 1] on the device; alpha fp32 [E], bias
     bf16 [E, N].  Rows outside every expert keep what `out` held (without `out`
     they are undefined)."""
-    if a.sf_layout != "128x4":
-        raise ValueError("the grouped GEMM needs activation scales in the 128x4 layout")
     return _grouped_gemm(True, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated)
 
 
