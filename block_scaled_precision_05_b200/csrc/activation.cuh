@@ -1,9 +1,12 @@
-// activation.cuh -- the activations of the fused GEMM epilogues, on fp32 values.
+// activation.cuh -- the activations of the fused GEMM epilogues, on fp32 values, two at a time.
 //
 // exp2 and the reciprocal are the hardware approximations (2^-22 relative error each, documented by PTX), so an
 // activation is within about 1e-6 of its formula relative to the result, far below half a step of bf16 (2^-9), and
 // below the rounding noise of an fp32 sum over K.  Tails keep their relative accuracy: nothing is computed as
 // 1 + tanh(x) or 1 + erf(x), which cancel for negative x.
+//
+// Both run on the special-function unit, 4 lanes a clock in each SM quarter, and an epilogue that applies an
+// activation is bound by it.  So two values share one reciprocal: 1/p = q / (pq), 1/q = p / (pq).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -24,28 +27,41 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// max(x, 0) that keeps NaN.
-__device__ __forceinline__ float act_relu(float x) { return x < 0.0f ? 0.0f : x; }
+// max that keeps NaN.
+__device__ __forceinline__ float max_nan(float x, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(c));
+  return y;
+}
 
-// x / (1 + e^-x).
-__device__ __forceinline__ float act_silu(float x) {
-  return x * rcp_approx(1.0f + ex2_approx(-1.44269504f * x));
+// x / (1 + 2^e(x)) for both, e(x) <= 60 so that the product of the denominators stays in range.
+__device__ __forceinline__ void logistic2(float& x0, float& x1, float e0, float e1) {
+  const float p = 1.0f + ex2_approx(e0), q = 1.0f + ex2_approx(e1);
+  const float r = rcp_approx(p * q);
+  x0 *= r * q;
+  x1 *= r * p;
+}
+
+// x / (1 + e^-x); below -40 as at -40 (-1.7e-16).
+__device__ __forceinline__ void silu2(float& x0, float& x1) {
+  x0 = max_nan(x0, -40.0f);
+  x1 = max_nan(x1, -40.0f);
+  logistic2(x0, x1, -1.44269504f * x0, -1.44269504f * x1);
 }
 
 // x/2 (1 + tanh u) = x / (1 + e^-2u), u = sqrt(2/pi) (x + 0.044715 x^3); the constants are 2 sqrt(2/pi) log2(e) and
-// that times 0.044715.
-__device__ __forceinline__ float act_gelu_tanh(float x) {
-  const float s = x * fmaf(0.102943240f, x * x, 2.30220820f);
-  return x * rcp_approx(1.0f + ex2_approx(-s));
+// that times 0.044715.  Below -7 as at -7 (-2.3e-15).
+__device__ __forceinline__ void gelu_tanh2(float& x0, float& x1) {
+  x0 = max_nan(x0, -7.0f);
+  x1 = max_nan(x1, -7.0f);
+  logistic2(x0, x1, -x0 * fmaf(0.102943240f, x0 * x0, 2.30220820f), -x1 * fmaf(0.102943240f, x1 * x1, 2.30220820f));
 }
 
 // x Phi(x) = max(x, 0) - |x| Q(|x|) with the normal tail Q(u) = e^(-u^2/2) P(1 / (1 + 0.23 u)).  P is a polynomial of
 // degree 8 fitted to e^(u^2/2) Q(u) over 0 <= u <= 14 by iteratively reweighted least squares (largest relative
 // error 4.8e-8; 6e-7 evaluated in fp32).  Beyond 14 the exponential is 0 in fp32; the clamp keeps |x| Q(|x|) at 0 for
 // infinite x.
-__device__ __forceinline__ float act_gelu(float x) {
-  const float u = fminf(fabsf(x), 32.0f);
-  const float t = rcp_approx(fmaf(0.23f, u, 1.0f));
+__device__ __forceinline__ float normal_tail(float u, float t) {
   float p = -0.0784672499f;
   p = fmaf(p, t, 0.290413111f);
   p = fmaf(p, t, -0.278124809f);
@@ -55,16 +71,29 @@ __device__ __forceinline__ float act_gelu(float x) {
   p = fmaf(p, t, 0.0857631117f);
   p = fmaf(p, t, 0.0923784301f);
   p = fmaf(p, t, -2.77608233e-05f);
-  return fmaf(-u * ex2_approx(-0.72134752f * u * u), p, act_relu(x));
+  return ex2_approx(-0.72134752f * u * u) * p;
+}
+
+__device__ __forceinline__ void gelu2(float& x0, float& x1) {
+  const float u0 = fminf(fabsf(x0), 32.0f), u1 = fminf(fabsf(x1), 32.0f);
+  const float p = fmaf(0.23f, u0, 1.0f), q = fmaf(0.23f, u1, 1.0f);
+  const float r = rcp_approx(p * q);
+  x0 = fmaf(-u0, normal_tail(u0, r * q), max_nan(x0, 0.0f));
+  x1 = fmaf(-u1, normal_tail(u1, r * p), max_nan(x1, 0.0f));
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate(float y) {
-  if constexpr (ACT == BSP_ACT_RELU) return act_relu(y);
-  else if constexpr (ACT == BSP_ACT_GELU) return act_gelu(y);
-  else if constexpr (ACT == BSP_ACT_GELU_TANH) return act_gelu_tanh(y);
-  else if constexpr (ACT == BSP_ACT_SILU) return act_silu(y);
-  else return y;
+__device__ __forceinline__ void activate2(float& x0, float& x1) {
+  if constexpr (ACT == BSP_ACT_RELU) {
+    x0 = max_nan(x0, 0.0f);
+    x1 = max_nan(x1, 0.0f);
+  } else if constexpr (ACT == BSP_ACT_GELU) {
+    gelu2(x0, x1);
+  } else if constexpr (ACT == BSP_ACT_GELU_TANH) {
+    gelu_tanh2(x0, x1);
+  } else if constexpr (ACT == BSP_ACT_SILU) {
+    silu2(x0, x1);
+  }
 }
 
 }  // namespace bsp

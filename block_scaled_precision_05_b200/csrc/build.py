@@ -21,8 +21,8 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
-SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "fused_gemm.cu"]
-HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "norm_stats.cuh", "tensor_maps.h"]
+SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "fused_gemm_nvfp4.cu", "fused_gemm_mxfp8.cu"]
+HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "fused_gemm.cuh", "norm_stats.cuh", "tensor_maps.h"]
 
 
 def nvcc() -> str:

@@ -1,4 +1,4 @@
-// fused_gemm.cu -- block-scaled GEMMs with an activation, a gate and a residual in the epilogue, dense or grouped by
+// fused_gemm.cuh -- block-scaled GEMMs with an activation, a gate and a residual in the epilogue, dense or grouped by
 // expert:
 //
 //   y[m, n] = alpha[e] * row_scale[m] * sum_k A(m,k) sA(m,k/g) B[e](n,k) sB[e](n,k/g) + bias[e, n]
@@ -21,6 +21,8 @@
 // (relays of a pair's follower), warps 4-7 scale factors, warps 8 and up the epilogue.  Every CTA builds the table of
 // the experts' tiles in shared memory from the offsets (a scan over the experts) and takes every gridDim-th tile:
 // nothing is read back to the host.
+#pragma once
+
 #include "activation.cuh"
 #include "bsp_device.cuh"
 #include "bsp_internal.h"
@@ -30,12 +32,21 @@ namespace bsp {
 namespace {
 
 constexpr int kMaxExperts = BSP_MAX_EXPERTS;  // the tile table's two words per expert in shared memory
+#ifndef FORCE
+#define FORCE 0
+#endif
+constexpr int kForce = FORCE;
+constexpr int kMaxSplit = 4;       // CTAs of a cluster that share a tile's K range
+constexpr int kMinSplitSteps = 8;  // K steps that each keeps at least
 
 struct FusedParams {
   int M, N, E;
   int num_kb;     // 128-byte steps of K
   int panels;     // weight panels per expert
   int group_m;    // token tiles per rasterisation group
+  int tn;         // most tokens per tile
+  int stages, stage_bytes, x_bytes;  // CG = 1: the ring's layout, by tn
+  int split;      // CG = 1: CTAs of a cluster sharing one tile's K range
   int act, gated;
   const int32_t* offsets;  // [E + 1], or NULL: one expert with every row
   const float* alpha;
@@ -48,11 +59,12 @@ struct FusedParams {
   uint32_t* err;
 };
 
-// CG = 2: CTA pairs, 256 weight rows x up to 256 tokens.  CG = 1: 128 weight rows x up to 64 tokens.
+// CG = 2: CTA pairs, 256 weight rows x up to 256 tokens.  CG = 1: 128 weight rows x up to 128 tokens, in a ring of as
+// many stages as fit for the launch's token tile.
 template <int KIND, int CG_>
 struct FCfg {
   static constexpr int CG = CG_;
-  static constexpr int TN = CG == 2 ? 256 : 64;          // most tokens per tile
+  static constexpr int TN = CG == 2 ? 256 : 128;         // most tokens per tile
   static constexpr int N_STEP = CG == 2 ? 32 : 16;       // granularity of the MMA's N
   static constexpr int X_ROWS = TN / CG;                 // token rows each CTA holds
   static constexpr int X_MAPS = X_ROWS / 32;             // sizes of the TMA box of tokens
@@ -70,25 +82,29 @@ struct FCfg {
   static constexpr int ACC_COLS = TN * ACC_BUFS;
   static constexpr int TMEM_COLS = 512;
   static constexpr int SF_WARPS = 4;
-  static constexpr int EPI_WARPS = CG == 2 ? 8 : 4;
+  static constexpr int EPI_WARPS = 8;
   static constexpr int FIRST_SF_WARP = 4, FIRST_EPI_WARP = 8;
   static constexpr int THREADS = (8 + EPI_WARPS) * 32;
-  static constexpr int STEPS = TN / (EPI_WARPS / 4) / 16;  // steps of 16 tokens per epilogue warp
-  // CTA pairs: warpgroups 0 and 1 hand registers to the epilogue, which holds 128 accumulator columns a thread.  (With
-  // 40 for the first, as in gemm.cu, its loops spill: 7% of a large GEMM.)
+  static constexpr int STEPS = TN / 2 / 16;  // steps of 16 tokens per epilogue warp
+  // Warpgroups 0 and 1 hand registers to the epilogue, which holds up to 128 accumulator columns a thread.  (With 40
+  // for the first, as in gemm.cu, its loops spill: 7% of a large GEMM.)
   static constexpr int WG0_REGS = 72, SF_REGS = 88, EPI_REGS = 176;
-  static_assert(CG == 1 || 128 * (WG0_REGS + SF_REGS + 2 * EPI_REGS) == THREADS * (65536 / THREADS), "register split");
-  static constexpr int STG_BYTES = 1024;  // staging: two buffers per warp, each a box of D for one TMA store
+  static_assert(128 * (WG0_REGS + SF_REGS + 2 * EPI_REGS) == THREADS * (65536 / THREADS), "register split");
+  static constexpr int STG_BYTES = 2048;  // staging: per warp, a box of D for one TMA store
   static constexpr int SCALE_BYTES = 16 * STEPS * 4;  // and its tokens' scales
   static constexpr int TABLE_BYTES = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int FIXED_BYTES = EPI_WARPS * (2 * STG_BYTES + SCALE_BYTES) + TABLE_BYTES + BAR_BYTES + 1024;
+  static constexpr int FIXED_BYTES = EPI_WARPS * (STG_BYTES + SCALE_BYTES) + TABLE_BYTES + BAR_BYTES + 1024;
   static constexpr int by_smem = (232448 - FIXED_BYTES) / STAGE_BYTES;
   static constexpr int by_tmem = (TMEM_COLS - ACC_COLS) / SF_COLS;
-  static constexpr int STAGES = by_smem < by_tmem ? (by_smem < 8 ? by_smem : 8) : (by_tmem < 8 ? by_tmem : 8);
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED_BYTES;
-  static_assert(STAGES >= 4 && SMEM_BYTES <= 232448 && ACC_COLS + STAGES * SF_COLS <= TMEM_COLS, "budget");
-  static_assert((4 * STAGES + 8) * 8 <= BAR_BYTES, "barrier space");
+  static constexpr int MAX_STAGES = by_tmem < 8 ? by_tmem : 8;
+  static constexpr int STAGES = by_smem < MAX_STAGES ? by_smem : MAX_STAGES;  // of the largest tile
+  static constexpr int RING_BYTES = CG == 2 ? STAGES * STAGE_BYTES : (232448 - FIXED_BYTES) / 1024 * 1024;
+  static constexpr int SMEM_BYTES = RING_BYTES + FIXED_BYTES;
+  static_assert(STAGES >= 4 && SMEM_BYTES <= 232448 && ACC_COLS + MAX_STAGES * SF_COLS <= TMEM_COLS, "budget");
+  static_assert((4 * MAX_STAGES + 8) * 8 <= BAR_BYTES, "barrier space");
+  // split K: a CTA's partial tile, one word per epilogue thread and accumulator register, in its drained ring
+  static_assert(CG == 2 || 16 * STEPS * EPI_WARPS * 32 * 4 <= RING_BYTES, "partial tile");
 };
 
 // TMA descriptors.  Tokens and their scales come in one box each per stage, of the smallest size that covers the
@@ -121,19 +137,19 @@ struct Table {
     lo = start + kMaxExperts + 1;
   }
 
+  __device__ __forceinline__ void build_dense(const FusedParams& p) {
+    if (threadIdx.x == 0) {
+      lo[0] = 0;
+      lo[1] = p.M;
+      start[0] = 0;
+      start[1] = (p.M + p.tn - 1) / p.tn * p.panels;
+    }
+  }
+
   // Offsets are clamped to [0, M], and one below an earlier one counts as that one, so that the experts' rows never
   // overlap whatever the array holds.  Called by the whole CTA.
-  template <int TN>
   __device__ __forceinline__ void build(const FusedParams& p) {
-    if (p.offsets == nullptr) {
-      if (threadIdx.x == 0) {
-        lo[0] = 0;
-        lo[1] = p.M;
-        start[0] = 0;
-        start[1] = (p.M + TN - 1) / TN * p.panels;
-      }
-      return;
-    }
+    const int TN = p.tn;
     for (int e = threadIdx.x; e <= p.E; e += blockDim.x) lo[e] = min(max(__ldg(p.offsets + e), 0), p.M);
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -167,12 +183,14 @@ struct Table {
       }
       if (lane == 0) start[p.E] = tiles;
     }
+    __syncthreads();
   }
 
   // Tile t: its expert by bisection, then token tiles within groups of group_m, fastest first, so that the CTAs that
   // run at once share weight panels and tokens in L2.  An expert's rows are shared out evenly over its tiles.
-  template <int TN, int N_STEP>
+  template <int N_STEP>
   __device__ __forceinline__ Tile get(int t, const FusedParams& p) const {
+    const int TN = p.tn;
     int a = 0, b = p.E;
     while (b - a > 1) {
       const int mid = (a + b) >> 1;
@@ -180,16 +198,20 @@ struct Table {
       else b = mid;
     }
     const int l = lo[a], rows = lo[a + 1] - l;
-    const int nt = (rows + TN - 1) / TN;
-    const int r = t - start[a];
-    const int per_group = p.group_m * p.panels;
-    const int g = r / per_group;
-    const int first = g * p.group_m;
-    const int size = min(p.group_m, nt - first);
-    const int rr = r - g * per_group;
-    const int nb = rr / size;
-    const int mt = first + rr - nb * size;
-    const int per = ((rows + nt - 1) / nt + N_STEP - 1) / N_STEP * N_STEP;
+    const int nt = rows <= TN ? 1 : (rows + TN - 1) / TN;
+    int r = t - start[a], first = 0, size = nt, per = (rows + N_STEP - 1) / N_STEP * N_STEP;
+    if (nt > 1) {  // (divisions are slow, and every role waits for its first tile)
+      per = ((rows + nt - 1) / nt + N_STEP - 1) / N_STEP * N_STEP;
+      if (nt > p.group_m) {
+        const int per_group = p.group_m * p.panels;
+        const int g = r / per_group;
+        first = g * p.group_m;
+        size = min(p.group_m, nt - first);
+        r -= g * per_group;
+      }
+    }
+    const int nb = size > 1 ? r / size : r;
+    const int mt = first + r - nb * size;
     Tile q;
     q.e = a;
     q.nb = nb;
@@ -273,17 +295,18 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   using C = FCfg<KIND, CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
-  uint8_t* table_mem = staging + C::EPI_WARPS * (2 * C::STG_BYTES + C::SCALE_BYTES);
+  uint8_t* staging = smem + C::RING_BYTES;
+  uint8_t* table_mem = staging + C::EPI_WARPS * (C::STG_BYTES + C::SCALE_BYTES);
   uint64_t* full = reinterpret_cast<uint64_t*>(table_mem + C::TABLE_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* sf_ready = empty + C::STAGES;
-  uint64_t* sf_local = sf_ready + C::STAGES;  // pair follower: its scale warps, per stage
-  uint64_t* acc_full = sf_local + C::STAGES;  // [ACC_BUFS]
+  uint64_t* empty = full + C::MAX_STAGES;
+  uint64_t* sf_ready = empty + C::MAX_STAGES;
+  uint64_t* sf_local = sf_ready + C::MAX_STAGES;  // pair follower: its scale warps, per stage
+  uint64_t* acc_full = sf_local + C::MAX_STAGES;  // [ACC_BUFS]
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* acc_local = acc_empty + 2;  // pair follower: its epilogue warps
   uint64_t* drain = acc_local + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* part_ready = drain + 1;  // split K: the partial tiles of every CTA of the cluster
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_ready + 1);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   Table table;
   table.carve(table_mem);
@@ -293,9 +316,17 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   const uint32_t rank = C::CG == 2 ? cluster_ctarank() : 0u;
   const bool leader = rank == 0u;
   constexpr uint32_t kPeerArrivals = C::CG == 2 ? 1u : 0u;  // the follower's relayed arrival
+  const int n_stages = C::CG == 2 ? C::STAGES : p.stages;
+  const int stage_bytes = C::CG == 2 ? C::STAGE_BYTES : p.stage_bytes;
+  const int x_bytes = C::CG == 2 ? C::X_BYTES : p.x_bytes;
+  // split K: CTA k_rank of a cluster of k_split takes K steps kb0 .. kb1 of the cluster's one tile
+  const int k_split = C::CG == 2 ? 1 : p.split;
+  const int k_rank = k_split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int kb0 = k_split > 1 ? p.num_kb * k_rank / k_split : 0;
+  const int kb1 = k_split > 1 ? p.num_kb * (k_rank + 1) / k_split : p.num_kb;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < n_stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&sf_ready[s], C::SF_WARPS + kPeerArrivals);
@@ -307,11 +338,12 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     }
     mbar_init(acc_local, C::EPI_WARPS);
     mbar_init(drain, 1);
+    mbar_init(part_ready, static_cast<uint32_t>(k_split * C::EPI_WARPS));
     *abort_flag = 0u;
     fence_barrier_init();
     prefetch_tensormap(&maps.w);
     prefetch_tensormap(&maps.sfw);
-    for (int i = 0; i < C::X_MAPS; ++i) prefetch_tensormap(&maps.x[i]);
+    for (int i = 0; i < p.tn / (32 * C::CG); ++i) prefetch_tensormap(&maps.x[i]);
     for (int i = 0; i < C::X_BANDS; ++i) prefetch_tensormap(&maps.sfx[i]);
     prefetch_tensormap(&maps.d);
   }
@@ -325,32 +357,34 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     }
   }
   __syncwarp();
+  if (p.offsets == nullptr) table.build_dense(p);
+  tc_fence_before_sync();
+  __syncwarp();
+  if (C::CG == 2 || k_split > 1)
+    cluster_sync();  // the peers' barriers are initialised before anything arrives on them
+  else
+    __syncthreads();
   // Set-up above overlaps the previous kernel under programmatic launch; every global access below comes after its
   // completion.
   grid_dependency_wait();
-  table.build<C::TN>(p);
-  tc_fence_before_sync();
-  __syncwarp();
-  if constexpr (C::CG == 2)
-    cluster_sync();  // the peer's barriers are initialised before anything arrives on them
-  else
-    __syncthreads();
+  if (p.offsets != nullptr) table.build(p);
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int num_tiles = table.start[p.E];
-  const int first_tile = static_cast<int>(blockIdx.x) / C::CG;
-  const int tile_step = static_cast<int>(gridDim.x) / C::CG;
+  const int first_tile = static_cast<int>(blockIdx.x) / (C::CG * k_split);
+  const int tile_step = static_cast<int>(gridDim.x) / (C::CG * k_split);
 
   if (warp < C::FIRST_SF_WARP) {
-    if constexpr (C::CG == 2) regs_dec<C::WG0_REGS>();
+    regs_dec<C::WG0_REGS>();
     if (warp == 0) {
       // ------------------------------------------------------------ producer
-      if (lane == 0) {
-        uint32_t stage = 0, phase = 0;
+      if (elect_one()) {
+        int stage = 0;
+        uint32_t phase = 0;
         uint32_t total = 0;  // stages issued
         bool ok = true;
         for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-          const Tile q = table.get<C::TN, C::N_STEP>(t, p);
+          const Tile q = table.get<C::N_STEP>(t, p);
           const int band = q.nb * C::CG + static_cast<int>(rank);  // of 128 weight rows
           const int x_rows = q.nmma / C::CG;
           const int x_row = q.row0 + static_cast<int>(rank) * x_rows;
@@ -359,13 +393,13 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
           const CUtensorMap* mx = &maps.x[x_box - 1];
           const CUtensorMap* msfx = &maps.sfx[x_bands - 1];
           const uint32_t tx = static_cast<uint32_t>(C::W_BYTES + x_box * 4096 + C::BAND_BYTES * (1 + x_bands));
-          for (int kb = 0; kb < p.num_kb; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
               ok = false;
               break;
             }
-            uint8_t* st = smem + stage * C::STAGE_BYTES;
-            uint8_t* sf = st + C::W_BYTES + C::X_BYTES;
+            uint8_t* st = smem + stage * stage_bytes;
+            uint8_t* sf = st + C::W_BYTES + x_bytes;
             mbar_arrive_expect_tx(&full[stage], tx);
             if (p.gated)
               tma_load_5d(st, &maps.w, &full[stage], kb * 128, 0, 0, band * 8, q.e);
@@ -375,7 +409,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             tma_load_4d(sf, &maps.sfw, &full[stage], 0, kb * C::ATOMS, band, q.e);
             tma_load_3d(sf + C::BAND_BYTES, msfx, &full[stage], 0, kb * C::ATOMS, q.row0 >> 7);
             ++total;
-            if (++stage == C::STAGES) {
+            if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -386,14 +420,15 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
           raise_error(p.err, kErrTimeout);
         }
         // Every issued copy must have landed before the CTA may exit.
-        for (uint32_t s = 0; s < C::STAGES; ++s)
-          if (total > s && !mbar_wait(&full[s], ((total - 1u - s) / C::STAGES) & 1u, nullptr))
+        for (uint32_t s = 0; s < n_stages; ++s)
+          if (total > s && !mbar_wait(&full[s], ((total - 1u - s) / n_stages) & 1u, nullptr))
             raise_error(p.err, kErrTimeout);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      if (lane == 0 && leader) {
-        uint32_t stage = 0, phase = 0;
+      if (leader && elect_one()) {
+        int stage = 0;
+        uint32_t phase = 0;
         bool ok = true;
         int it = 0;
         auto commit = [&](uint64_t* bar) {
@@ -409,7 +444,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             return mbar_wait(bar, par, abort_flag);
         };
         for (int t = first_tile; t < num_tiles && ok; t += tile_step, ++it) {
-          const Tile q = table.get<C::TN, C::N_STEP>(t, p);
+          const Tile q = table.get<C::N_STEP>(t, p);
           const int buf = it % C::ACC_BUFS;
           const uint32_t acc = tmem + static_cast<uint32_t>(buf * C::TN);
           if (!wait_shared(&acc_empty[buf], (static_cast<uint32_t>(it / C::ACC_BUFS) & 1u) ^ 1u)) {
@@ -417,20 +452,20 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             break;
           }
           tc_fence_after_sync();
-          for (int kb = 0; kb < p.num_kb; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!wait_shared(&sf_ready[stage], phase)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint32_t sbase = smem_u32(smem + stage * C::STAGE_BYTES);
+            const uint32_t sbase = smem_u32(smem + stage * stage_bytes);
             const uint32_t sfw_t = tmem + C::ACC_COLS + stage * C::SF_COLS;
             const uint32_t sfx_t = sfw_t + C::SFW_COLS;
             const uint64_t wdesc = desc_kmajor_sw128(sbase);
             const uint64_t xdesc = desc_kmajor_sw128(sbase + C::W_BYTES);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t accumulate = (kb > 0 || kk > 0) ? 1u : 0u;
+              const uint32_t accumulate = (kb > kb0 || kk > 0) ? 1u : 0u;
               if constexpr (KIND == kNVF4) {
                 const uint32_t idesc = idesc_nvf4(128 * C::CG, q.nmma);
                 const uint32_t sfx_k = sfx_t + static_cast<uint32_t>(C::X_WORDS * kk);
@@ -447,7 +482,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
               }
             }
             commit(&empty[stage]);
-            if (++stage == C::STAGES) {
+            if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -462,7 +497,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
         // No MMA may still be running when tensor memory is freed.
         commit(drain);
         if (!mbar_wait(drain, 0u, nullptr)) raise_error(p.err, kErrTimeout);
-      } else if (lane == 0) {
+      } else if (!leader && lane == 0) {
         // pair follower: its MMAs are issued by the leader, whose last commit arrives here too
         if (!mbar_wait(drain, 0u, nullptr)) raise_error(p.err, kErrTimeout);
       }
@@ -471,15 +506,16 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
       bool ok = true;
       if (warp == 2) {
         const uint32_t peer = mapa_shared(smem_u32(sf_ready), 0u);
-        uint32_t stage = 0, phase = 0;
+        int stage = 0;
+        uint32_t phase = 0;
         for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-          for (int kb = 0; kb < p.num_kb; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&sf_local[stage], phase, abort_flag)) {
               ok = false;
               break;
             }
             mbar_arrive_remote_relaxed(peer + 8u * stage);
-            if (++stage == C::STAGES) {
+            if (++stage == n_stages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -503,15 +539,16 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     }
   } else if (warp < C::FIRST_EPI_WARP) {
     // ------------------------------------------------------------ scale factors
-    if constexpr (C::CG == 2) regs_dec<C::SF_REGS>();
+    regs_dec<C::SF_REGS>();
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    uint32_t stage = 0, phase = 0;
+    int stage = 0;
+        uint32_t phase = 0;
     bool ok = true;
     uint64_t* sf_mine = leader ? sf_ready : sf_local;
     // gated: the accumulator's rows are the weight's in the order of the epilogue (gated_row)
     const int w_line = p.gated ? gated_row(static_cast<int>(lane)) : static_cast<int>(lane);
     for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-      const Tile q = table.get<C::TN, C::N_STEP>(t, p);
+      const Tile q = table.get<C::N_STEP>(t, p);
       // Scale row i of the tile is row (row0 & 127) + i of the loaded bands.  Line `lane` of tensor memory takes the
       // words of rows lane + 32 j, which all sit in line (row0 + lane) & 31 of the tiles, at word `shift` + j (plus
       // one in the lanes where row0 + lane carries into the next 32 rows) of the bands' words one after another.
@@ -521,19 +558,19 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
       auto stages = [&](auto variant) {
         constexpr int kShift = decltype(variant)::kShift;
         constexpr bool kWide = decltype(variant)::kWide;
-        for (int kb = 0; kb < p.num_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&full[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           copy_scales<KIND, CG, kShift, kWide>(tmem + lane_base + C::ACC_COLS + stage * C::SF_COLS,
-                                               smem + stage * C::STAGE_BYTES + C::W_BYTES + C::X_BYTES, w_line, line,
+                                               smem + stage * stage_bytes + C::W_BYTES + x_bytes, w_line, line,
                                                carry);
           tmem_st_wait();
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sf_mine[stage]);
-          if (++stage == C::STAGES) {
+          if (++stage == n_stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -565,24 +602,23 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     // A lane of tensor memory is a weight row, a column a token.  A warp reads its 32 rows x up to 16 STEPS tokens
     // into registers as 8 x 8 fragments (thread t: row t / 4, tokens 2 (t % 4) and the next), hands the accumulator
     // back, finishes the values in fp32, rounds them once and turns them over on the way to shared memory (stmatrix
-    // with a transpose), 16 tokens x 32 columns of D at a time, from where they go out as one TMA store.  (16-byte
+    // with a transpose), 32 tokens x 32 columns of D at a time, from where they go out as one TMA store.  (16-byte
     // stores from the lanes took 25% longer over the whole GEMM; turning fp32 values over through shared memory and
     // storing 8 tokens at a time took twice as long as the MMAs at K = 1536.)  The box that holds an expert's last
     // rows is stored by the lanes, row by row: the rows after them belong to another expert.
-    if constexpr (C::CG == 2) regs_inc<C::EPI_REGS>();
+    regs_inc<C::EPI_REGS>();
     const int ew = warp - C::FIRST_EPI_WARP;
     const int quarter = warp & 3;
     const int half = ew >> 2;
     const int fr = static_cast<int>(lane) >> 2, fc = 2 * (static_cast<int>(lane) & 3);  // fragment row, first token
     uint64_t* acc_mine = leader ? acc_empty : acc_local;
     const uint64_t evict_first = l2_policy_evict_first();
-    float* scales = reinterpret_cast<float*>(staging + C::EPI_WARPS * 2 * C::STG_BYTES) + ew * 16 * C::STEPS;
-    uint32_t seq = 0;  // boxes of this warp (picks the staging buffer)
+    float* scales = reinterpret_cast<float*>(staging + C::EPI_WARPS * C::STG_BYTES) + ew * 16 * C::STEPS;
     int it = 0;
     for (int t = first_tile; t < num_tiles; t += tile_step, ++it) {
-      const Tile q = table.get<C::TN, C::N_STEP>(t, p);
+      const Tile q = table.get<C::N_STEP>(t, p);
       const int buf = it % C::ACC_BUFS;
-      const int width = C::CG == 2 ? q.nmma / 2 : q.nmma;  // tokens per epilogue warp
+      const int width = (q.nmma / 2 + 31) & ~31;           // tokens per epilogue warp, whole boxes of D
       const int tok0 = half * width;                       // this warp's first token of the tile
       const int col0 = (q.nb * C::CG + static_cast<int>(rank)) * 128 + quarter * 32;  // first weight row
       const float alpha = p.alpha != nullptr ? __ldg(p.alpha + q.e) : 1.0f;
@@ -602,6 +638,17 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             (p.row_scale != nullptr && tk < q.cnt) ? __fmul_rn(alpha, __ldg(p.row_scale + q.row0 + tk)) : alpha;
       }
       __syncwarp();
+      if constexpr (kRes) {  // this warp's rows of the residual on their way into L2 while the MMAs run
+        const int c0 = p.gated ? col0 >> 1 : col0;
+        if (c0 < (p.gated ? p.N >> 1 : p.N)) {
+#pragma unroll
+          for (int j = 0; j < 16 * C::STEPS; j += 32) {
+            const int tk = tok0 + j + static_cast<int>(lane);
+            if (tk < q.cnt && j + static_cast<int>(lane) < width)
+              prefetch_l2(static_cast<const uint8_t*>(p.residual) + ((q.row0 + tk) * p.ld_res + c0) * (kF32 ? 4 : 2));
+          }
+        }
+      }
       const uint32_t par = static_cast<uint32_t>(it / C::ACC_BUFS) & 1u;
       const bool got = C::CG == 2 ? mbar_wait_cluster(&acc_full[buf], par, abort_flag)
                                   : mbar_wait(&acc_full[buf], par, abort_flag);
@@ -625,9 +672,52 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(C::CG == 2 ? acc_mine : &acc_empty[buf]);
 
+      // the steps of this warp, one bit each
+      const int lim = min(width, q.cnt - tok0);
+      uint32_t steps = lim > 0 ? (1u << ((lim + 15) >> 4)) - 1u : 0u;
+      if (C::CG == 1 && k_split > 1) {
+        // Split K: every CTA leaves its partial tile in its own ring (all of its loads have been consumed: the cluster
+        // has one tile), register by register, and finishes the steps that fall to it with the sum over the cluster in
+        // rank order, whichever CTA came first.
+        float* part = reinterpret_cast<float*>(smem) + ew * 32 + lane;
+#pragma unroll
+        for (int s = 0; s < C::STEPS; ++s) {
+          if (steps >> s & 1u) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              part[(16 * s + i) * C::EPI_WARPS * 32] = __uint_as_float(r[i >> 3][s / 4][8 * (s & 3) + (i & 7)]);
+          }
+        }
+        __syncwarp();
+        if (static_cast<int>(lane) < k_split) mbar_arrive_remote(mapa_shared(smem_u32(part_ready), lane));
+        if (!mbar_wait_cluster(part_ready, 0u, abort_flag)) {
+          *abort_flag = 1u;
+          raise_error(p.err, kErrTimeout);
+          break;
+        }
+        uint32_t mine = 0;
+#pragma unroll
+        for (int s = 0; s < C::STEPS; ++s) {
+          if ((steps >> s & 1u) && ((s >> 1) * 2 + half) % k_split == k_rank) {
+            mine |= 1u << s;
+            float sum[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+            for (int c = 0; c < k_split; ++c) {
+              const uint32_t peer = mapa_shared(smem_u32(part), static_cast<uint32_t>(c));
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                sum[i] = __fadd_rn(sum[i], ld_shared_cluster_f1(peer + 4u * (16 * s + i) * C::EPI_WARPS * 32));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i >> 3][s / 4][8 * (s & 3) + (i & 7)] = __float_as_uint(sum[i]);
+          }
+        }
+        steps = mine;
+      }
+
       // One straight line of code per activation and gate: the unrolled steps (the accumulator is in registers, so
       // they cannot be a loop) would otherwise carry every branch.
-      const int lim = min(width, q.cnt - tok0);
       auto finish = [&](auto kind) {
         constexpr int kAct = decltype(kind)::kAct;
         constexpr bool kGated = decltype(kind)::kGated;
@@ -635,135 +725,178 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
         const int cols = kGated ? p.N >> 1 : p.N;
         const int d_col0 = kGated ? col0 >> 1 : col0;
 
-        // A box of D in a staging buffer: rows of kRow bytes, 16-byte chunks swizzled as the TMA store reads them.
-        auto chunk = [](int row, int c, int row_bytes) {
-          return row * row_bytes + 16 * (c ^ (row_bytes == 128 ? row & 7 : row_bytes == 64 ? (row >> 1) & 3 : (row >> 2) & 1));
+        // A box of D in the staging buffer: kRows tokens, rows of kRow bytes in 16-byte chunks, swizzled as the TMA
+        // store reads them.
+        constexpr int kSize = kF32 ? 4 : 2;
+        constexpr int kRow = kCols * kSize;
+        constexpr int kRows = kF32 ? 16 : 32;
+        constexpr int kChunks = kRows * (kRow / 16);
+        static_assert(kRows * kRow <= C::STG_BYTES && kChunks % 32 == 0, "box");
+        uint8_t* box = staging + ew * C::STG_BYTES;
+        auto chunk = [](int row, int c) {
+          return row * kRow + 16 * (c ^ (kRow == 128 ? row & 7 : kRow == 64 ? (row >> 1) & 3 : (row >> 2) & 1));
         };
-        auto open_box = [&]() {
-          if (lane == 0) bulk_wait_read_allow<1>();  // the store from this buffer, two boxes back, has read it
-          __syncwarp();
-          return staging + (ew * 2 + (seq++ & 1)) * C::STG_BYTES;
-        };
-        // the residual's box, one 16-byte chunk per lane and turn, into the buffer
-        auto fill_box = [&](uint8_t* box, int tb, int rows, int row_bytes, int esize) {
-          const int per_row = row_bytes >> 4;
-#pragma unroll 1
-          for (int c = static_cast<int>(lane); c < rows * per_row; c += 32) {
-            const int row = c / per_row, cc = c - row * per_row;
-            const int col = d_col0 + cc * (16 / esize);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (tb + row < q.cnt && col < cols)
-              v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) +
-                                                  ((q.row0 + tb + row) * p.ld_res + col) * esize);
-            *reinterpret_cast<uint4*>(box + chunk(row, cc, row_bytes)) = v;
-          }
-          __syncwarp();
-        };
-        auto close_box = [&](uint8_t* box, int tb, int rows, int row_bytes, int esize) {
-          if (tb + rows <= q.cnt) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && d_col0 < cols) tma_store_2d_hint(&maps.d, box, d_col0, q.row0 + tb, evict_first);
-          } else {
-            __syncwarp();
-            const int per_row = row_bytes >> 4;
-#pragma unroll 1
-            for (int c = static_cast<int>(lane); c < rows * per_row; c += 32) {
-              const int row = c / per_row, cc = c - row * per_row;
-              const int col = d_col0 + cc * (16 / esize);
-              if (tb + row < q.cnt && col < cols)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.D) + ((q.row0 + tb + row) * p.ld_d + col) * esize) =
-                    *reinterpret_cast<const uint4*>(box + chunk(row, cc, row_bytes));
+        // this lane's chunks: column l_col of rows l_row + i kLaneRows
+        constexpr int kLaneRows = 32 / (kRow / 16);
+        const int l_chunk = static_cast<int>(lane) % (kRow / 16), l_row = static_cast<int>(lane) / (kRow / 16);
+        const int l_col = d_col0 + l_chunk * (16 / kSize);
+        const bool l_ok = l_col < cols;
+
+        // z[o][n][u]: octet of tokens o, 8-column block n, token fc + u
+        constexpr int kBlocks = kGated ? 2 : 4;
+        auto values = [&](int s, float (&z)[2][kBlocks][2]) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const float2 sc2 = *reinterpret_cast<const float2*>(scales + 16 * s + 8 * o + fc);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float sc = u == 0 ? sc2.x : sc2.y;
+              const int at = 4 * ((2 * s + o) & 7) + u;
+              float y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = __fmaf_rn(__uint_as_float(r[i >> 1][s / 4][at + 2 * (i & 1)]), sc, bias[i]);
+              if constexpr (kGated) {
+                activate2<kAct>(y[0], y[2]);
+                z[o][0][u] = y[0] * y[1];
+                z[o][1][u] = y[2] * y[3];
+              } else {
+                activate2<kAct>(y[0], y[1]);
+                activate2<kAct>(y[2], y[3]);
+#pragma unroll
+                for (int i = 0; i < kBlocks; ++i) z[o][i][u] = y[i];
+              }
             }
           }
-          if (lane == 0) bulk_commit_group();  // one group per box, empty or not: open_box counts boxes
+        };
+        // shared address of this lane's row of a group of four 8 x 8 matrices (lane l: row l % 8 of matrix l / 8):
+        // the four blocks of octet `o` of the box, or gated both blocks of octets o and o + 1
+        auto matrix_at = [&](int o) {
+          const int m = static_cast<int>(lane) >> 3, l = static_cast<int>(lane) & 7;
+          return smem_u32(box) + (kGated ? chunk(8 * (o + (m >> 1)) + l, m & 1) : chunk(8 * o + l, m));
         };
 
 #pragma unroll
-        for (int s = 0; s < C::STEPS; ++s) {
-          const int tb = tok0 + 16 * s;  // first token of the step
-          if (16 * s < lim) {  // warp-uniform
-            // z[o][n][u]: octet of tokens o, 8-column block n, token fc + u
-            constexpr int kBlocks = kGated ? 2 : 4;
-            float z[2][kBlocks][2];
+        for (int s0 = 0; s0 < C::STEPS; s0 += kRows / 16) {
+          const int tb = tok0 + 16 * s0;  // first token of the box
+          if (steps >> s0 & 1u) {         // warp-uniform
+            constexpr int kSteps = kRows / 16;
+            uint32_t w[kSteps][2][kBlocks];  // bf16 pairs of tokens
+            if constexpr (!kRes && !kF32) {
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const float2 sc2 = *reinterpret_cast<const float2*>(scales + 16 * s + 8 * o + fc);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float sc = u == 0 ? sc2.x : sc2.y;
-                const int at = 4 * ((2 * s + o) & 7) + u;
-                float y[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  y[i] = __fmaf_rn(__uint_as_float(r[i >> 1][s / 4][at + 2 * (i & 1)]), sc, bias[i]);
-#pragma unroll
-                for (int i = 0; i < kBlocks; ++i)
-                  z[o][i][u] = kGated ? activate<kAct>(y[2 * i & 3]) * y[(2 * i + 1) & 3] : activate<kAct>(y[i]);
-              }
-            }
-            if constexpr (!kF32) {
-              constexpr int kRow = 2 * kCols;
-              uint8_t* box = open_box();
-              // lane l addresses row l % 8 of matrix l / 8 of a group of four
-              const int m = static_cast<int>(lane) >> 3;
-              uint32_t at[kGated ? 1 : 2];
-              if constexpr (kGated) {
-                at[0] = smem_u32(box) + chunk(8 * (m >> 1) + (lane & 7), m & 1, kRow);  // (octet, block)
-              } else {
-                at[0] = smem_u32(box) + chunk(lane & 7, m, kRow);
-                at[1] = smem_u32(box) + chunk(8 + (lane & 7), m, kRow);
-              }
-              uint32_t w[2][kBlocks];
-              if constexpr (kRes) {
-                fill_box(box, tb, 16, kRow, 2);
-                if constexpr (kGated) {
-                  ldmatrix_x4_trans(at[0], w[0][0], w[0][1], w[1][0], w[1][1]);
-                } else {
-                  ldmatrix_x4_trans(at[0], w[0][0], w[0][1], w[0][2 % kBlocks], w[0][3 % kBlocks]);
-                  ldmatrix_x4_trans(at[1], w[1][0], w[1][1], w[1][2 % kBlocks], w[1][3 % kBlocks]);
-                }
-                __syncwarp();  // every lane has read before the result takes the residual's place
+              for (int i = 0; i < kSteps; ++i) {
+                float z[2][kBlocks][2];
+                values(s0 + i, z);
 #pragma unroll
                 for (int o = 0; o < 2; ++o)
 #pragma unroll
-                  for (int i = 0; i < kBlocks; ++i) {
-                    z[o][i][0] += bf16_bits_to_f32(w[o][i] & 0xFFFFu);
-                    z[o][i][1] += bf16_bits_to_f32(w[o][i] >> 16);
+                  for (int n = 0; n < kBlocks; ++n) w[i][o][n] = pack_bf16x2(z[o][n][0], z[o][n][1]);
+              }
+            }
+            if (elect_one()) bulk_wait_read_all();  // the store of the previous box has read the buffer
+            __syncwarp();
+            if constexpr (kRes && !kF32) {
+              uint4 v[kChunks / 32];
+              const uint8_t* src = static_cast<const uint8_t*>(p.residual) +
+                                   ((q.row0 + tb + l_row) * p.ld_res + l_col) * kSize;
+#pragma unroll
+              for (int i = 0; i < kChunks / 32; ++i) {
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
+                  v[i] = *reinterpret_cast<const uint4*>(src + i * (kLaneRows * kSize) * p.ld_res);
+              }
+#pragma unroll
+              for (int i = 0; i < kChunks / 32; ++i)
+                *reinterpret_cast<uint4*>(box + chunk(l_row + i * kLaneRows, l_chunk)) = v[i];
+              __syncwarp();
+            }
+            if constexpr (!kF32) {
+              if constexpr (kRes) {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                  float z[2][kBlocks][2];
+                  values(s0 + i, z);
+                  if constexpr (kGated) {
+                    ldmatrix_x4_trans(matrix_at(2 * i), w[i][0][0], w[i][0][1], w[i][1][0], w[i][1][1]);
+                  } else {
+#pragma unroll
+                    for (int o = 0; o < 2; ++o)
+                      ldmatrix_x4_trans(matrix_at(2 * i + o), w[i][o][0], w[i][o][1], w[i][o][2 % kBlocks],
+                                        w[i][o][3 % kBlocks]);
                   }
-              }
 #pragma unroll
-              for (int o = 0; o < 2; ++o)
+                  for (int o = 0; o < 2; ++o)
 #pragma unroll
-                for (int i = 0; i < kBlocks; ++i) w[o][i] = pack_bf16x2(z[o][i][0], z[o][i][1]);
-              if constexpr (kGated) {
-                stmatrix_x4_trans(at[0], w[0][0], w[0][1], w[1][0], w[1][1]);
-              } else {
-                stmatrix_x4_trans(at[0], w[0][0], w[0][1], w[0][2 % kBlocks], w[0][3 % kBlocks]);
-                stmatrix_x4_trans(at[1], w[1][0], w[1][1], w[1][2 % kBlocks], w[1][3 % kBlocks]);
-              }
-              close_box(box, tb, 16, kRow, 2);
-            } else {
-              constexpr int kRow = 4 * kCols;
-              constexpr int kRows = kGated ? 16 : 8;  // a box is 1 KB
-#pragma unroll
-              for (int o0 = 0; o0 < 2; o0 += kRows / 8) {
-                if (tb + 8 * o0 < q.cnt) {  // warp-uniform
-                  uint8_t* box = open_box();
-                  if constexpr (kRes) fill_box(box, tb + 8 * o0, kRows, kRow, 4);
-#pragma unroll
-                  for (int o = o0; o < o0 + kRows / 8; ++o)
-#pragma unroll
-                    for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-                      for (int u = 0; u < 2; ++u) {
-                        const int row = 8 * (o - o0) + fc + u, n = 8 * i + fr;
-                        float* at = reinterpret_cast<float*>(box + chunk(row, n >> 2, kRow)) + (n & 3);
-                        *at = kRes ? z[o][i][u] + *at : z[o][i][u];
-                      }
-                  close_box(box, tb + 8 * o0, kRows, kRow, 4);
+                    for (int n = 0; n < kBlocks; ++n)
+                      w[i][o][n] = pack_bf16x2(z[o][n][0] + bf16_bits_to_f32(w[i][o][n] & 0xFFFFu),
+                                               z[o][n][1] + bf16_bits_to_f32(w[i][o][n] >> 16));
                 }
               }
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) {
+                if constexpr (kGated) {
+                  stmatrix_x4_trans(matrix_at(2 * i), w[i][0][0], w[i][0][1], w[i][1][0], w[i][1][1]);
+                } else {
+#pragma unroll
+                  for (int o = 0; o < 2; ++o)
+                    stmatrix_x4_trans(matrix_at(2 * i + o), w[i][o][0], w[i][o][1], w[i][o][2 % kBlocks],
+                                      w[i][o][3 % kBlocks]);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kSteps; ++i) {
+                float z[2][kBlocks][2];
+                values(s0 + i, z);
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                  for (int n = 0; n < kBlocks; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                      // row 16 i + 8 o + fc + u, column 8 n + fr: n moves the chunk by an exclusive or with 2 n
+                      float* at = reinterpret_cast<float*>(box + ((chunk(fc + u, fr >> 2) + 4 * (fr & 3)) ^ (32 * n)) +
+                                                           (16 * i + 8 * o) * kRow);
+                      *at = z[o][n][u];
+                    }
+              }
+            }
+            if constexpr (kRes && kF32) {
+              // fp32 rows are whole 128-byte lines: the lanes add the residual and store them themselves (there are no
+              // registers for a residual in the fragments' order beside the accumulator)
+              const float* src = static_cast<const float*>(p.residual) + (q.row0 + tb + l_row) * p.ld_res + l_col;
+              float* dst = static_cast<float*>(p.D) + (q.row0 + tb + l_row) * p.ld_d + l_col;
+              float4 v[kChunks / 32];
+#pragma unroll
+              for (int i = 0; i < kChunks / 32; ++i) {
+                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
+                  v[i] = *reinterpret_cast<const float4*>(src + i * kLaneRows * p.ld_res);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < kChunks / 32; ++i) {
+                const float4 d = *reinterpret_cast<const float4*>(box + chunk(l_row + i * kLaneRows, l_chunk));
+                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
+                  __stcs(reinterpret_cast<float4*>(dst + i * kLaneRows * p.ld_d),
+                         make_float4(d.x + v[i].x, d.y + v[i].y, d.z + v[i].z, d.w + v[i].w));
+              }
+              __syncwarp();  // the box has been read
+            } else if (tb + kRows <= q.cnt) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (elect_one()) {
+                if (d_col0 < cols) tma_store_2d_hint(&maps.d, box, d_col0, q.row0 + tb, evict_first);
+                bulk_commit_group();
+              }
+            } else {
+              __syncwarp();
+              uint8_t* dst = static_cast<uint8_t*>(p.D) + ((q.row0 + tb + l_row) * p.ld_d + l_col) * kSize;
+#pragma unroll
+              for (int i = 0; i < kChunks / 32; ++i)
+                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
+                  *reinterpret_cast<uint4*>(dst + i * (kLaneRows * kSize) * p.ld_d) =
+                      *reinterpret_cast<const uint4*>(box + chunk(l_row + i * kLaneRows, l_chunk));
             }
           }
         }
@@ -786,14 +919,14 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (elect_one()) bulk_wait_read_all();
     __syncwarp();
   }
 
   tc_fence_before_sync();
   __syncwarp();
-  if constexpr (C::CG == 2)
-    cluster_sync();  // no CTA of the pair leaves while the other may still signal it
+  if (C::CG == 2 || k_split > 1)
+    cluster_sync();  // no CTA leaves while another may still signal it or read its partial tile
   else
     __syncthreads();
   if (warp == 1) {
@@ -810,6 +943,15 @@ struct FusedArgs {
   const uint8_t *A, *sfA, *B, *sfB;
   int64_t row_bytes, tiles_per_band;
 };
+
+// CTAs per tile: a split of K over a cluster when the tiles alone leave at least half of the SMs idle and every CTA
+// keeps at least kMinSplitSteps 128-byte steps.
+int fused_split(const DeviceInfo& dev, int64_t tiles, int num_kb) {
+  int64_t s = dev.sm_count / tiles;
+  s = s < kMaxSplit ? s : kMaxSplit;
+  s = s < num_kb / kMinSplitSteps ? s : num_kb / kMinSplitSteps;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
 
 template <int KIND, int CG, bool kF32, bool kRes>
 int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cudaStream_t stream) {
@@ -828,19 +970,31 @@ int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cud
     return st;
   if ((st = encode_expert_scales(&maps.sfw, a.sfB, p.E, ceil_div(p.N, 128), a.tiles_per_band, C::ATOMS)) != BSP_OK)
     return st;
-  for (int i = 0; i < C::X_MAPS; ++i)
+  for (int i = 0; i < (p.tn / CG + 31) / 32; ++i)
     if ((st = encode_operand(&maps.x[i], a.A, p.M, a.row_bytes, 32 * (i + 1))) != BSP_OK) return st;
   for (int i = 0; i < C::X_BANDS; ++i)
     if ((st = encode_scales(&maps.sfx[i], a.sfA, ceil_div(p.M, 128), a.tiles_per_band, C::ATOMS, i + 1)) != BSP_OK)
       return st;
-  if ((st = encode_rows(&maps.d, p.D, p.M, p.gated ? p.N / 2 : p.N, p.ld_d, kF32, kF32 && !p.gated ? 8 : 16,
+  if ((st = encode_rows(&maps.d, p.D, p.M, p.gated ? p.N / 2 : p.N, p.ld_d, kF32, kF32 ? 16 : 32,
                         p.gated ? 16 : 32)) != BSP_OK)
     return st;
 
   p.num_kb = static_cast<int>(ceil_div(a.row_bytes, 128));
   p.panels = static_cast<int>(ceil_div(p.N, 128 * CG));
-  const int64_t most = (ceil_div(p.M, C::TN) + (p.E < p.M ? p.E : p.M)) * p.panels;  // tiles, at most
-  if (most > (1ll << 30)) return BSP_ERR_INVALID_ARG;
+  int64_t groups = dev.sm_count / CG;
+  p.split = 1;
+  if constexpr (CG == 1) {
+    p.x_bytes = static_cast<int>(round_up(p.tn, 32)) * 128;
+    p.stage_bytes = static_cast<int>(round_up(C::W_BYTES + p.x_bytes + C::BAND_BYTES * (1 + C::X_BANDS), 1024));
+    p.stages = C::RING_BYTES / p.stage_bytes;
+    if (p.stages > C::MAX_STAGES) p.stages = C::MAX_STAGES;
+    if (p.offsets == nullptr) {
+      p.split = fused_split(dev, ceil_div(p.M, p.tn) * p.panels, p.num_kb);
+      groups /= p.split;
+    }
+  }
+  const int64_t most = (ceil_div(p.M, p.tn) + (p.offsets == nullptr ? 0 : p.E < p.M ? p.E : p.M)) * p.panels;
+  if (most > (1ll << 30)) return BSP_ERR_INVALID_ARG;  // tiles, at most
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.blockDim = dim3(C::THREADS, 1, 1);
@@ -851,31 +1005,37 @@ int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int64_t groups = dev.sm_count / CG;
-  if constexpr (CG == 2) {
+  const int cluster = CG * p.split;
+  if (cluster > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    static int resident[64] = {};  // pairs resident at once, per device
-    if (resident[dev.id] == 0) {
-      cfg.gridDim = dim3(static_cast<unsigned>(groups * 2), 1, 1);
-      int r = 0;
-      if (cudaOccupancyMaxActiveClusters(&r, kernel, &cfg) != cudaSuccess) return launch_status();
-      if (r < 1) return BSP_ERR_CUDA;  // a pair does not fit: nothing launched
-      resident[dev.id] = r;
+    static int resident[64][kMaxSplit + 1] = {};  // clusters resident at once, per device and size
+    int& r = resident[dev.id][cluster];
+    if (r == 0) {
+      cfg.gridDim = dim3(static_cast<unsigned>(groups * cluster), 1, 1);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return launch_status();
+      if (n < 1) return BSP_ERR_CUDA;  // a cluster does not fit: nothing launched
+      r = n;
     }
-    if (groups > resident[dev.id]) groups = resident[dev.id];
+    if (groups > r) groups = r;
+    if (p.split > 1 && groups < most) {  // a split cluster takes one tile only
+      p.split = 1;
+      groups = dev.sm_count;
+      cfg.numAttrs = 1;
+    }
   }
   if (most < groups) groups = most;
   // Token tiles per rasterisation group, as in gemm.cu: weights well inside L2: just enough token tiles that the CTAs
   // running at once cover every panel; large weights: about 24 MiB of tokens per group.
   const int64_t b_bytes = static_cast<int64_t>(p.N) * a.row_bytes * 17 / 16;
   int64_t g = b_bytes < (32ll << 20) ? ceil_div(2 * groups, p.panels)
-                                     : (24ll << 20) / (static_cast<int64_t>(C::TN) * a.row_bytes * 17 / 16);
+                                     : (24ll << 20) / (static_cast<int64_t>(p.tn) * a.row_bytes * 17 / 16);
   p.group_m = static_cast<int>(g < 8 ? 8 : g > (1 << 20) ? (1 << 20) : g);
-  cfg.gridDim = dim3(static_cast<unsigned>(groups * CG), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(groups * CG * p.split), 1, 1);
   if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) return launch_status();
   return launch_status();
 }
@@ -934,48 +1094,15 @@ int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
   p.D = D;
   p.ld_d = ld_d;
   p.err = dev.err_word;
-  // CTA pairs for experts of more than 64 rows on average
-  if (ceil_div(M, E) > 64) return launch_fused<KIND, 2>(dev, a, p, d_dtype == BSP_OUT_F32, stream);
-  return launch_fused<KIND, 1>(dev, a, p, d_dtype == BSP_OUT_F32, stream);
+  const bool f32 = d_dtype == BSP_OUT_F32;
+  if (kForce == 2 || (kForce == 0 && ceil_div(M, E) > 128)) {
+    p.tn = 256;
+    return launch_fused<KIND, 2>(dev, a, p, f32, stream);
+  }
+  const int64_t rows = ceil_div(M, E);
+  p.tn = rows <= 16 ? 32 : rows <= 48 ? 64 : 128;
+  return launch_fused<KIND, 1>(dev, a, p, f32, stream);
 }
 
 }  // namespace
 }  // namespace bsp
-
-extern "C" {
-
-int nvfp4_gemm_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB, int64_t M, int64_t N,
-                     int64_t K, const float* alpha, const float* row_scale, const uint16_t* bias, int activation,
-                     int gated, const void* residual, int64_t ld_residual, void* D, int d_dtype, int64_t ld_d,
-                     bsp_stream_t stream) {
-  return bsp::run_fused<bsp::kNVF4>(A, sfA, B, sfB, nullptr, 1, M, N, K, alpha, row_scale, bias, activation, gated,
-                                    residual, ld_residual, D, d_dtype, ld_d, stream);
-}
-
-int mxfp8_gemm_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB, int64_t M, int64_t N,
-                     int64_t K, const float* alpha, const uint16_t* bias, int activation, int gated,
-                     const void* residual, int64_t ld_residual, void* D, int d_dtype, int64_t ld_d,
-                     bsp_stream_t stream) {
-  return bsp::run_fused<bsp::kMXF8>(A, sfA, B, sfB, nullptr, 1, M, N, K, alpha, nullptr, bias, activation, gated,
-                                    residual, ld_residual, D, d_dtype, ld_d, stream);
-}
-
-int nvfp4_grouped_gemm(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
-                       const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K, const float* alpha,
-                       const float* row_scale, const uint16_t* bias, int activation, int gated, void* D, int d_dtype,
-                       int64_t ld_d, bsp_stream_t stream) {
-  if (offsets == nullptr && M > 0 && N > 0) return BSP_ERR_INVALID_ARG;
-  return bsp::run_fused<bsp::kNVF4>(A, sfA, B, sfB, offsets, E, M, N, K, alpha, row_scale, bias, activation, gated,
-                                    nullptr, 0, D, d_dtype, ld_d, stream);
-}
-
-int mxfp8_grouped_gemm(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB,
-                       const int32_t* offsets, int64_t E, int64_t M, int64_t N, int64_t K, const float* alpha,
-                       const uint16_t* bias, int activation, int gated, void* D, int d_dtype, int64_t ld_d,
-                       bsp_stream_t stream) {
-  if (offsets == nullptr && M > 0 && N > 0) return BSP_ERR_INVALID_ARG;
-  return bsp::run_fused<bsp::kMXF8>(A, sfA, B, sfB, offsets, E, M, N, K, alpha, nullptr, bias, activation, gated,
-                                    nullptr, 0, D, d_dtype, ld_d, stream);
-}
-
-}  // extern "C"
