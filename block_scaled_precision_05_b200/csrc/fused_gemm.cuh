@@ -32,12 +32,8 @@ namespace bsp {
 namespace {
 
 constexpr int kMaxExperts = BSP_MAX_EXPERTS;  // the tile table's two words per expert in shared memory
-#ifndef FORCE
-#define FORCE 0
-#endif
-constexpr int kForce = FORCE;
-constexpr int kMaxSplit = 4;       // CTAs of a cluster that share a tile's K range
-constexpr int kMinSplitSteps = 8;  // K steps that each keeps at least
+constexpr int kMaxSplit = 4;        // CTAs of a cluster that share a tile's K range
+constexpr int kMinSplitSteps = 16;  // K steps that each keeps at least
 
 struct FusedParams {
   int M, N, E;
@@ -376,8 +372,11 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
 
   if (warp < C::FIRST_SF_WARP) {
     regs_dec<C::WG0_REGS>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ producer
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------------------------ producers
+      // Warp 0 loads the weights' and tokens' codes, warp 3 their scales: a thread takes about 40 clocks to issue a
+      // TMA load, and a stage of a narrow tile has MMAs for 180 only.  Both wait for the same empty slot; warp 0's
+      // arrival expects the bytes of all four loads.
       if (elect_one()) {
         int stage = 0;
         uint32_t phase = 0;
@@ -399,15 +398,18 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
               break;
             }
             uint8_t* st = smem + stage * stage_bytes;
-            uint8_t* sf = st + C::W_BYTES + x_bytes;
-            mbar_arrive_expect_tx(&full[stage], tx);
-            if (p.gated)
-              tma_load_5d(st, &maps.w, &full[stage], kb * 128, 0, 0, band * 8, q.e);
-            else
-              tma_load_3d(st, &maps.w, &full[stage], kb * 128, band * 128, q.e);
-            tma_load_2d(st + C::W_BYTES, mx, &full[stage], kb * 128, x_row);
-            tma_load_4d(sf, &maps.sfw, &full[stage], 0, kb * C::ATOMS, band, q.e);
-            tma_load_3d(sf + C::BAND_BYTES, msfx, &full[stage], 0, kb * C::ATOMS, q.row0 >> 7);
+            if (warp == 0) {
+              mbar_arrive_expect_tx(&full[stage], tx);
+              if (p.gated)
+                tma_load_5d(st, &maps.w, &full[stage], kb * 128, 0, 0, band * 8, q.e);
+              else
+                tma_load_3d(st, &maps.w, &full[stage], kb * 128, band * 128, q.e);
+              tma_load_2d(st + C::W_BYTES, mx, &full[stage], kb * 128, x_row);
+            } else {
+              uint8_t* sf = st + C::W_BYTES + x_bytes;
+              tma_load_4d(sf, &maps.sfw, &full[stage], 0, kb * C::ATOMS, band, q.e);
+              tma_load_3d(sf + C::BAND_BYTES, msfx, &full[stage], 0, kb * C::ATOMS, q.row0 >> 7);
+            }
             ++total;
             if (++stage == n_stages) {
               stage = 0;
@@ -502,39 +504,42 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
         if (!mbar_wait(drain, 0u, nullptr)) raise_error(p.err, kErrTimeout);
       }
     } else if (C::CG == 2 && !leader && lane == 0) {
-      // pair follower: warp 2 relays each stage's scales to the leader, warp 3 each released accumulator
-      bool ok = true;
-      if (warp == 2) {
-        const uint32_t peer = mapa_shared(smem_u32(sf_ready), 0u);
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&sf_local[stage], phase, abort_flag)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_remote_relaxed(peer + 8u * stage);
-            if (++stage == n_stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
+      // pair follower, warp 2: relays to the leader each stage's scales and each released accumulator, whichever
+      // comes (the scales run up to a ring ahead of the accumulators)
+      const uint32_t peer_sf = mapa_shared(smem_u32(sf_ready), 0u), peer_acc = mapa_shared(smem_u32(acc_empty), 0u);
+      int acc_left = first_tile < num_tiles ? (num_tiles - first_tile + tile_step - 1) / tile_step : 0;
+      int64_t sf_left = static_cast<int64_t>(acc_left) * p.num_kb;
+      int stage = 0;
+      uint32_t sf_phase = 0, acc_phase = 0, idle = 0;
+      uint64_t t0 = 0;
+      while (sf_left > 0 || acc_left > 0) {
+        bool got = false;
+        if (sf_left > 0 && mbar_test_wait(smem_u32(&sf_local[stage]), sf_phase)) {
+          mbar_arrive_remote_relaxed(peer_sf + 8u * stage);
+          --sf_left;
+          if (++stage == n_stages) {
+            stage = 0;
+            sf_phase ^= 1u;
           }
+          got = true;
         }
-      } else {
-        const uint32_t peer = mapa_shared(smem_u32(acc_empty), 0u);
-        int it = 0;
-        for (int t = first_tile; t < num_tiles && ok; t += tile_step, ++it) {
-          if (!mbar_wait(acc_local, static_cast<uint32_t>(it) & 1u, abort_flag)) {
-            ok = false;
+        if (acc_left > 0 && mbar_test_wait(smem_u32(acc_local), acc_phase)) {
+          mbar_arrive_remote_relaxed(peer_acc);
+          --acc_left;
+          acc_phase ^= 1u;
+          got = true;
+        }
+        if (got) {
+          idle = 0;
+        } else if ((++idle & 63u) == 0u) {
+          const uint64_t now = globaltimer_ns();
+          if (idle == 64u) t0 = now;
+          if (*abort_flag || now - t0 > kWaitLimitNs) {
+            *abort_flag = 1u;
+            raise_error(p.err, kErrTimeout);
             break;
           }
-          mbar_arrive_remote_relaxed(peer);
         }
-      }
-      if (!ok) {
-        *abort_flag = 1u;
-        raise_error(p.err, kErrTimeout);
       }
     }
   } else if (warp < C::FIRST_EPI_WARP) {
@@ -542,7 +547,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     regs_dec<C::SF_REGS>();
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int stage = 0;
-        uint32_t phase = 0;
+    uint32_t phase = 0;
     bool ok = true;
     uint64_t* sf_mine = leader ? sf_ready : sf_local;
     // gated: the accumulator's rows are the weight's in the order of the epilogue (gated_row)
@@ -945,7 +950,8 @@ struct FusedArgs {
 };
 
 // CTAs per tile: a split of K over a cluster when the tiles alone leave at least half of the SMs idle and every CTA
-// keeps at least kMinSplitSteps 128-byte steps.
+// keeps at least kMinSplitSteps 128-byte steps.  Measured (us, split / whole): N = 5120, K = 13824 (54 steps), M = 16:
+// 14.6 / 18.3; N = 5120, K = 5120 (20 steps): two of 10 steps 11.5 / 10.9; N = 1536, K = 1536: 8.3 / 5.9.
 int fused_split(const DeviceInfo& dev, int64_t tiles, int num_kb) {
   int64_t s = dev.sm_count / tiles;
   s = s < kMaxSplit ? s : kMaxSplit;
@@ -1049,6 +1055,38 @@ int launch_fused(const DeviceInfo& dev, const FusedArgs& a, const FusedParams& p
                     : launch_variant<KIND, CG, false, false>(dev, a, p, stream);
 }
 
+// The form and the token tile, from the sizes and the experts' mean row count (their own are on the device).
+//  - CTA pairs (256 x 256 tiles) once the 128 x 128 tiles of single CTAs no longer fit in one wave: the pair's operands
+//    cost half the bandwidth (us, pairs / single: M = 4096, N = 13824, K = 5120: 121 / 162; M = 256, same weights:
+//    18.2 / 20.5), but its epilogue and its larger tiles take longer where everything runs at once (M = 256, N = 5120,
+//    K = 13824: 28.6 / 23.0).  Up to 8 K steps the single form's second accumulator, which overlaps the epilogue with
+//    the next tile, is worth up to three waves (M = 4096, N = K = 1536: 16.4 / 14.2).
+//    Experts: single up to a mean of 64 rows (128 experts of 1536 x 2048: 50.4 / 53.1 at 64 rows, 60.5 / 71.7 at 128;
+//    8 of 13824 x 5120: 60.9 / 58.3 and 66.3 / 78.9).
+//  - Single CTAs, token tile 32, 64 or 128: narrow tiles leave room for a deeper ring, but cost a pass over the weight
+//    each.  Dense: the smallest that covers M; with up to 8 K steps, where a tile's time is its epilogue's, the
+//    smallest whose tiles fit in one wave (M = 256, N = K = 1536: 6.9 against 7.4 at 128).  Experts: 32 up to a mean
+//    of 8 rows, 64 up to 16 (128 experts: 39.9 / 40.6 / 41.4 at 8 rows, 47.1 / 42.8 / 43.8 at 16).
+bool choose_tile(const DeviceInfo& dev, FusedParams& p, int64_t num_kb) {
+  const int64_t panels = ceil_div(p.N, 128), waves = num_kb <= 8 ? 3 : 1;
+  if (p.offsets == nullptr) {
+    if (ceil_div(p.M, 128) * panels > waves * dev.sm_count) {
+      p.tn = 256;
+      return true;
+    }
+    for (p.tn = 32; p.tn < 128; p.tn *= 2)
+      if (p.M <= p.tn || (num_kb <= 8 && ceil_div(p.M, p.tn) * panels <= dev.sm_count)) break;
+    return false;
+  }
+  const int64_t rows = ceil_div(p.M, p.E);
+  if (rows > 64) {
+    p.tn = 256;
+    return true;
+  }
+  p.tn = rows <= 8 ? 32 : rows <= 16 ? 64 : 128;
+  return false;
+}
+
 template <int KIND>
 int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB, const int32_t* offsets,
               int64_t E, int64_t M, int64_t N, int64_t K, const float* alpha, const float* row_scale,
@@ -1095,13 +1133,8 @@ int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
   p.ld_d = ld_d;
   p.err = dev.err_word;
   const bool f32 = d_dtype == BSP_OUT_F32;
-  if (kForce == 2 || (kForce == 0 && ceil_div(M, E) > 128)) {
-    p.tn = 256;
-    return launch_fused<KIND, 2>(dev, a, p, f32, stream);
-  }
-  const int64_t rows = ceil_div(M, E);
-  p.tn = rows <= 16 ? 32 : rows <= 48 ? 64 : 128;
-  return launch_fused<KIND, 1>(dev, a, p, f32, stream);
+  const bool pairs = choose_tile(dev, p, ceil_div(a.row_bytes, 128));
+  return pairs ? launch_fused<KIND, 2>(dev, a, p, f32, stream) : launch_fused<KIND, 1>(dev, a, p, f32, stream);
 }
 
 }  // namespace
