@@ -435,29 +435,12 @@ def _activation_code(activation: str | None) -> int:
     return ACTIVATIONS[activation]
 
 
-def _check_operand(what: str, codes: torch.Tensor, sf: torch.Tensor, shape: tuple, sf_bytes: int) -> None:
-    """A hand-made operand whose buffers are smaller than its sizes say would be read out of range."""
-    if codes.dtype is not torch.uint8 or codes.shape != shape or not codes.is_contiguous():
-        raise ValueError(f"{what}: expected contiguous uint8 codes of shape {shape}, got {tuple(codes.shape)}")
-    if sf.dtype is not torch.uint8 or sf.numel() != sf_bytes or not sf.is_contiguous():
-        raise ValueError(f"{what}: expected {sf_bytes} contiguous scale bytes, got {sf.numel()}")
+_OUT_CODES = {torch.bfloat16: nat.BSP_OUT_BF16, torch.float32: nat.BSP_OUT_F32}
 
 
 def _check_vector(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int) -> None:
     if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
-
-
-def _one_device(first: torch.Tensor, *ts: torch.Tensor | None) -> int:
-    """The operands' device, whose current stream the launch goes to."""
-    index = first.get_device()
-    for t in ts:
-        if t is not None and t.get_device() != index:
-            _require_cuda(first, *ts)
-            raise ValueError(f"operands on different devices: {first.device} and {t.device}")
-    if index < 0:
-        _require_cuda(first)
-    return index
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -479,67 +462,86 @@ def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, act
     if act < 0:
         _activation_code(activation)
     if fp4:
-        acodes, bcodes = a.codes, b.codes
+        ca, cb = a.codes, b.codes
         if a.sf_layout != "128x4" or (offsets is None and b.sf_layout != "128x4"):
             raise ValueError("a fused epilogue or a grouped GEMM needs scales in the 128x4 layout")
     else:
-        acodes, bcodes = a.q, b.q
-    K = a.K
+        ca, cb = a.q, b.q
+    sfa, sfb, K = a.sf, b.sf, a.K
     if K != b.K:
         raise ValueError("A and B disagree on K")
-    M = acodes.shape[0]
-    width = K // 2 if fp4 else K
-    tiles = ((K // (16 if fp4 else 32) + 3) // 4) * 512  # scale bytes per 128 rows
+    # sizes; a hand-made operand whose buffers are smaller than they say would be read out of range
+    M = ca.shape[0]
+    width, tiles = (K >> 1, ((K >> 4) + 3) // 4 * 512) if fp4 else (K, ((K >> 5) + 3) // 4 * 512)
+    shape = cb.shape
     if offsets is None:
-        E, N = 1, bcodes.shape[0]
-        shape = (N, width)
+        E, N = 1, shape[0]
+        ok = shape == (N, width)
     else:
-        E, N = bcodes.shape[0], bcodes.shape[1]
-        shape = (E, N, width)
-    index = _one_device(acodes, a.sf, bcodes, b.sf, offsets, alpha, row_scale, bias, residual, out)
-    _check_operand("A", acodes, a.sf, (M, width), (M + 127) // 128 * tiles)
-    _check_operand("B", bcodes, b.sf, shape, E * ((N + 127) // 128) * tiles)
+        E, N = shape[0], shape[1]
+        ok = shape == (E, N, width)
+    if not (ok and cb.dtype is torch.uint8 and cb.is_contiguous()):
+        raise ValueError(f"B: expected contiguous uint8 codes {'[N, ' if offsets is None else '[E, N, '}{width}], "
+                         f"got {tuple(shape)}")
+    if ca.shape != (M, width) or ca.dtype is not torch.uint8 or not ca.is_contiguous():
+        raise ValueError(f"A: expected contiguous uint8 codes [M, {width}], got {tuple(ca.shape)}")
+    if sfa.numel() != (M + 127) // 128 * tiles or sfa.dtype is not torch.uint8 or not sfa.is_contiguous():
+        raise ValueError(f"A: expected {(M + 127) // 128 * tiles} contiguous scale bytes, got {sfa.numel()}")
+    if sfb.numel() != E * ((N + 127) // 128) * tiles or sfb.dtype is not torch.uint8 or not sfb.is_contiguous():
+        raise ValueError(f"B: expected {E * ((N + 127) // 128) * tiles} contiguous scale bytes, got {sfb.numel()}")
+    cols = N
+    if gated:
+        if N % 2 != 0:
+            raise ValueError("a gated weight has an even number of rows")
+        cols = N // 2
+    if out is None and out_dtype in _OUT_CODES:
+        out = ca.new_empty((M, cols), dtype=out_dtype)
+    else:
+        out, _ = _out(M, cols, out_dtype, ca.device, out)
+    # the operands' device, whose current stream the launch goes to; the optional operands
+    index = ca.get_device()
+    same = index == cb.get_device() == sfa.get_device() == sfb.get_device() == out.get_device() and index >= 0
+    pal = prs = pbi = pre = pof = None
+    ld_res = 0
     if alpha is not None:
         _check_vector("alpha", alpha, torch.float32, E)
+        same, pal = same and alpha.get_device() == index, alpha.data_ptr()
     if row_scale is not None:
         _check_vector("row_scale", row_scale, torch.float32, M)
+        same, prs = same and row_scale.get_device() == index, row_scale.data_ptr()
     if bias is not None:
         _check_vector("bias", bias, torch.bfloat16, E * N)
-    if gated and N % 2 != 0:
-        raise ValueError("a gated weight has an even number of rows")
-    cols = N // 2 if gated else N
-    if out is None and out_dtype in (torch.bfloat16, torch.float32):
-        out = torch.empty((M, cols), dtype=out_dtype, device=acodes.device)
-    else:
-        out, _ = _out(M, cols, out_dtype, acodes.device, out)
-    ld_res = 0
+        same, pbi = same and bias.get_device() == index, bias.data_ptr()
+    if offsets is not None:
+        same, pof = same and offsets.get_device() == index, offsets.data_ptr()
     if residual is not None:
         if residual.dtype is not out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
             raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
-        ld_res = residual.stride(0)
-        if (residual.data_ptr() != out.data_ptr() or ld_res != out.stride(0)) and _overlap(residual, out):
-            raise ValueError("residual may be the output itself, but must not overlap it otherwise")
+        same, pre, ld_res = same and residual.get_device() == index, residual.data_ptr(), residual.stride(0)
+    pd, ld = out.data_ptr(), out.stride(0)
+    if not same:
+        _require_cuda(ca, sfa, cb, sfb, offsets, alpha, row_scale, bias, residual, out)
+        raise ValueError("operands on different devices")
+    if pre is not None and (pre != pd or ld_res != ld) and _overlap(residual, out):
+        raise ValueError("residual may be the output itself, but must not overlap it otherwise")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
 
-    L, d_dtype, ld, stream = nat.lib(), nat.BSP_OUT_F32 if out.dtype is torch.float32 else nat.BSP_OUT_BF16, \
-        out.stride(0), _stream(index)
-    pa, psa, pb, psb, pd = acodes.data_ptr(), a.sf.data_ptr(), bcodes.data_ptr(), b.sf.data_ptr(), out.data_ptr()
-    palpha, pbias, gated = _ptr(alpha), _ptr(bias), int(gated)
+    L, stream, d_dtype = nat.lib(), _stream(index), _OUT_CODES[out.dtype]
     if offsets is None:
         if fp4:
-            st = L.nvfp4_gemm_fused(pa, psa, pb, psb, M, N, K, palpha, _ptr(row_scale), pbias, act, gated,
-                                    _ptr(residual), ld_res, pd, d_dtype, ld, stream)
+            st = L.nvfp4_gemm_fused(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), M, N, K, pal, prs,
+                                    pbi, act, 1 if gated else 0, pre, ld_res, pd, d_dtype, ld, stream)
         else:
-            st = L.mxfp8_gemm_fused(pa, psa, pb, psb, M, N, K, palpha, pbias, act, gated, _ptr(residual), ld_res, pd,
-                                    d_dtype, ld, stream)
+            st = L.mxfp8_gemm_fused(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), M, N, K, pal, pbi,
+                                    act, 1 if gated else 0, pre, ld_res, pd, d_dtype, ld, stream)
     elif fp4:
-        st = L.nvfp4_grouped_gemm(pa, psa, pb, psb, offsets.data_ptr(), E, M, N, K, palpha, _ptr(row_scale), pbias, act,
-                                  gated, pd, d_dtype, ld, stream)
+        st = L.nvfp4_grouped_gemm(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal,
+                                  prs, pbi, act, 1 if gated else 0, pd, d_dtype, ld, stream)
     else:
-        st = L.mxfp8_grouped_gemm(pa, psa, pb, psb, offsets.data_ptr(), E, M, N, K, palpha, pbias, act, gated, pd,
-                                  d_dtype, ld, stream)
+        st = L.mxfp8_grouped_gemm(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal,
+                                  pbi, act, 1 if gated else 0, pd, d_dtype, ld, stream)
     if st:
         nat.check(st, "fused GEMM" if offsets is None else "grouped GEMM")
     return out
@@ -670,7 +672,7 @@ def mxfp8_quantize_experts(w: torch.Tensor) -> MXFP8Experts:
 
 
 def _grouped_gemm(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated):
-    E = b.experts
+    E = (b.codes if fp4 else b.q).shape[0]
     if not 1 <= E <= nat.BSP_MAX_EXPERTS:
         raise ValueError(f"1 to {nat.BSP_MAX_EXPERTS} experts, got {E}")
     if offsets is None or offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
