@@ -32,6 +32,7 @@ namespace bsp {
 namespace {
 
 constexpr int kMaxExperts = BSP_MAX_EXPERTS;  // the tile table's two words per expert in shared memory
+constexpr int kListed = 64;         // tiles of a CTA that it looks up before the roles start
 constexpr int kMaxSplit = 4;        // CTAs of a cluster that share a tile's K range
 constexpr int kMinSplitSteps = 16;  // K steps that each keeps at least
 
@@ -89,8 +90,9 @@ struct FCfg {
   static constexpr int STG_BYTES = 2048;  // staging: per warp, a box of D for one TMA store
   static constexpr int SCALE_BYTES = 16 * STEPS * 4;  // and its tokens' scales
   static constexpr int TABLE_BYTES = (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;
+  static constexpr int LIST_BYTES = kListed * 16;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int FIXED_BYTES = EPI_WARPS * (STG_BYTES + SCALE_BYTES) + TABLE_BYTES + BAR_BYTES + 1024;
+  static constexpr int FIXED_BYTES = EPI_WARPS * (STG_BYTES + SCALE_BYTES) + TABLE_BYTES + LIST_BYTES + BAR_BYTES + 1024;
   static constexpr int by_smem = (232448 - FIXED_BYTES) / STAGE_BYTES;
   static constexpr int by_tmem = (TMEM_COLS - ACC_COLS) / SF_COLS;
   static constexpr int MAX_STAGES = by_tmem < 8 ? by_tmem : 8;
@@ -293,7 +295,8 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + C::RING_BYTES;
   uint8_t* table_mem = staging + C::EPI_WARPS * (C::STG_BYTES + C::SCALE_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(table_mem + C::TABLE_BYTES);
+  int4* list = reinterpret_cast<int4*>(table_mem + C::TABLE_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(table_mem + C::TABLE_BYTES + C::LIST_BYTES);
   uint64_t* empty = full + C::MAX_STAGES;
   uint64_t* sf_ready = empty + C::MAX_STAGES;
   uint64_t* sf_local = sf_ready + C::MAX_STAGES;  // pair follower: its scale warps, per stage
@@ -369,6 +372,22 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   const int num_tiles = table.start[p.E];
   const int first_tile = static_cast<int>(blockIdx.x) / (C::CG * k_split);
   const int tile_step = static_cast<int>(gridDim.x) / (C::CG * k_split);
+  // This CTA's first tiles are looked up once, side by side: a lookup takes 500 to 1000 clocks (a bisection and
+  // divisions, between instructions that have to be fetched again), and one in front of every tile of every role cost
+  // 2400 a tile in the epilogue (128 experts, 32768 x 2048 x 768: 72 us against 60).
+  if (threadIdx.x < kListed) {
+    const int64_t t = first_tile + static_cast<int64_t>(threadIdx.x) * tile_step;
+    if (t < num_tiles) {
+      const Tile q = table.get<C::N_STEP>(static_cast<int>(t), p);
+      list[threadIdx.x] = make_int4(q.e, q.nb, q.row0, q.cnt);
+    }
+  }
+  __syncthreads();
+  auto tile_at = [&](int t, int it) {
+    if (it >= kListed) return table.get<C::N_STEP>(t, p);
+    const int4 v = list[it];
+    return Tile{v.x, v.y, v.z, v.w, (v.w + C::N_STEP - 1) / C::N_STEP * C::N_STEP};
+  };
 
   if (warp < C::FIRST_SF_WARP) {
     regs_dec<C::WG0_REGS>();
@@ -382,8 +401,8 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
         uint32_t phase = 0;
         uint32_t total = 0;  // stages issued
         bool ok = true;
-        for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-          const Tile q = table.get<C::N_STEP>(t, p);
+        for (int t = first_tile, it = 0; t < num_tiles && ok; t += tile_step, ++it) {
+          const Tile q = tile_at(t, it);
           const int band = q.nb * C::CG + static_cast<int>(rank);  // of 128 weight rows
           const int x_rows = q.nmma / C::CG;
           const int x_row = q.row0 + static_cast<int>(rank) * x_rows;
@@ -446,7 +465,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             return mbar_wait(bar, par, abort_flag);
         };
         for (int t = first_tile; t < num_tiles && ok; t += tile_step, ++it) {
-          const Tile q = table.get<C::N_STEP>(t, p);
+          const Tile q = tile_at(t, it);
           const int buf = it % C::ACC_BUFS;
           const uint32_t acc = tmem + static_cast<uint32_t>(buf * C::TN);
           if (!wait_shared(&acc_empty[buf], (static_cast<uint32_t>(it / C::ACC_BUFS) & 1u) ^ 1u)) {
@@ -552,8 +571,8 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     uint64_t* sf_mine = leader ? sf_ready : sf_local;
     // gated: the accumulator's rows are the weight's in the order of the epilogue (gated_row)
     const int w_line = p.gated ? gated_row(static_cast<int>(lane)) : static_cast<int>(lane);
-    for (int t = first_tile; t < num_tiles && ok; t += tile_step) {
-      const Tile q = table.get<C::N_STEP>(t, p);
+    for (int t = first_tile, it = 0; t < num_tiles && ok; t += tile_step, ++it) {
+      const Tile q = tile_at(t, it);
       // Scale row i of the tile is row (row0 & 127) + i of the loaded bands.  Line `lane` of tensor memory takes the
       // words of rows lane + 32 j, which all sit in line (row0 + lane) & 31 of the tiles, at word `shift` + j (plus
       // one in the lanes where row0 + lane carries into the next 32 rows) of the bands' words one after another.
@@ -621,7 +640,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     float* scales = reinterpret_cast<float*>(staging + C::EPI_WARPS * C::STG_BYTES) + ew * 16 * C::STEPS;
     int it = 0;
     for (int t = first_tile; t < num_tiles; t += tile_step, ++it) {
-      const Tile q = table.get<C::N_STEP>(t, p);
+      const Tile q = tile_at(t, it);
       const int buf = it % C::ACC_BUFS;
       const int width = (q.nmma / 2 + 31) & ~31;           // tokens per epilogue warp, whole boxes of D
       const int tok0 = half * width;                       // this warp's first token of the tile
