@@ -501,8 +501,7 @@ def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, act
     # the operands' device, whose current stream the launch goes to; the optional operands
     index = ca.get_device()
     same = index == cb.get_device() == sfa.get_device() == sfb.get_device() == out.get_device() and index >= 0
-    pal = prs = pbi = pre = pof = None
-    ld_res = 0
+    pal = prs = pbi = pre = pof = ld_res = 0  # 0: NULL
     if alpha is not None:
         _check_vector("alpha", alpha, torch.float32, E)
         same, pal = same and alpha.get_device() == index, alpha.data_ptr()
@@ -519,31 +518,23 @@ def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, act
             raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
         same, pre, ld_res = same and residual.get_device() == index, residual.data_ptr(), residual.stride(0)
     pd, ld = out.data_ptr(), out.stride(0)
+    if M == 1:  # one row has no stride: a broadcast or sliced tensor's is anything
+        ld = ld_res = (cols + 7) // 8 * 8
     if not same:
         _require_cuda(ca, sfa, cb, sfb, offsets, alpha, row_scale, bias, residual, out)
         raise ValueError("operands on different devices")
-    if pre is not None and (pre != pd or ld_res != ld) and _overlap(residual, out):
+    if pre and (pre != pd or ld_res != ld) and _overlap(residual, out):
         raise ValueError("residual may be the output itself, but must not overlap it otherwise")
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
 
-    L, stream, d_dtype = nat.lib(), _stream(index), _OUT_CODES[out.dtype]
-    if offsets is None:
-        if fp4:
-            st = L.nvfp4_gemm_fused(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), M, N, K, pal, prs,
-                                    pbi, act, 1 if gated else 0, pre, ld_res, pd, d_dtype, ld, stream)
-        else:
-            st = L.mxfp8_gemm_fused(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), M, N, K, pal, pbi,
-                                    act, 1 if gated else 0, pre, ld_res, pd, d_dtype, ld, stream)
-    elif fp4:
-        st = L.nvfp4_grouped_gemm(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal,
-                                  prs, pbi, act, 1 if gated else 0, pd, d_dtype, ld, stream)
-    else:
-        st = L.mxfp8_grouped_gemm(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal,
-                                  pbi, act, 1 if gated else 0, pd, d_dtype, ld, stream)
+    desc = nat.pack_fused_desc(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal, prs,
+                               pbi, act, 1 if gated else 0, pre, ld_res, pd, _OUT_CODES[out.dtype], ld)
+    L = nat.lib()
+    st = (L.nvfp4_gemm_fused if fp4 else L.mxfp8_gemm_fused)(desc, _stream(index))
     if st:
-        nat.check(st, "fused GEMM" if offsets is None else "grouped GEMM")
+        nat.check(st, "nvfp4_gemm_fused" if fp4 else "mxfp8_gemm_fused")
     return out
 
 

@@ -662,16 +662,36 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             (p.row_scale != nullptr && tk < q.cnt) ? __fmul_rn(alpha, __ldg(p.row_scale + q.row0 + tk)) : alpha;
       }
       __syncwarp();
-      if constexpr (kRes) {  // this warp's rows of the residual on their way into L2 while the MMAs run
+      // A residual: this warp's rows on their way into L2 while the MMAs run, and the first box of them into registers
+      // (16-byte chunks, as the boxes of D below are laid out); the next box is loaded while one is finished (in fp32 there
+      // are no registers for that: a box is loaded when its sums are in shared memory).
+      constexpr int kResRows = kF32 ? 16 : 32;
+      uint4 res[4];
+      const int res_row_chunks = (kF32 ? 8 : 4) >> p.gated;
+      auto load_residual = [&](int tb) {
+        const int row = static_cast<int>(lane) / res_row_chunks, step = 32 / res_row_chunks;
+        const int col = (p.gated ? col0 >> 1 : col0) + static_cast<int>(lane) % res_row_chunks * (kF32 ? 4 : 8);
+        const bool ok = col < (p.gated ? p.N >> 1 : p.N);
+        const uint8_t* src = static_cast<const uint8_t*>(p.residual) +
+                             ((q.row0 + tb + row) * p.ld_res + col) * (kF32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          res[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (ok && (i < 2 || !p.gated) && tb + row + i * step < q.cnt)
+            res[i] = *reinterpret_cast<const uint4*>(src + i * step * (kF32 ? 4 : 2) * p.ld_res);
+        }
+      };
+      if constexpr (kRes) {
         const int c0 = p.gated ? col0 >> 1 : col0;
         if (c0 < (p.gated ? p.N >> 1 : p.N)) {
 #pragma unroll
-          for (int j = 0; j < 16 * C::STEPS; j += 32) {
+          for (int j = kF32 ? 0 : kResRows; j < 16 * C::STEPS; j += 32) {
             const int tk = tok0 + j + static_cast<int>(lane);
             if (tk < q.cnt && j + static_cast<int>(lane) < width)
               prefetch_l2(static_cast<const uint8_t*>(p.residual) + ((q.row0 + tk) * p.ld_res + c0) * (kF32 ? 4 : 2));
           }
         }
+        if constexpr (!kF32) load_residual(tok0);
       }
       const uint32_t par = static_cast<uint32_t>(it / C::ACC_BUFS) & 1u;
       const bool got = C::CG == 2 ? mbar_wait_cluster(&acc_full[buf], par, abort_flag)
@@ -803,6 +823,7 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
 #pragma unroll
         for (int s0 = 0; s0 < C::STEPS; s0 += kRows / 16) {
           const int tb = tok0 + 16 * s0;  // first token of the box
+          if (kRes && !kF32 && !(steps >> s0 & 1u) && (steps >> (s0 + kRows / 16) & 1u)) load_residual(tb + kRows);
           if (steps >> s0 & 1u) {         // warp-uniform
             constexpr int kSteps = kRows / 16;
             uint32_t w[kSteps][2][kBlocks];  // bf16 pairs of tokens
@@ -820,18 +841,10 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             if (elect_one()) bulk_wait_read_all();  // the store of the previous box has read the buffer
             __syncwarp();
             if constexpr (kRes && !kF32) {
-              uint4 v[kChunks / 32];
-              const uint8_t* src = static_cast<const uint8_t*>(p.residual) +
-                                   ((q.row0 + tb + l_row) * p.ld_res + l_col) * kSize;
-#pragma unroll
-              for (int i = 0; i < kChunks / 32; ++i) {
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
-                  v[i] = *reinterpret_cast<const uint4*>(src + i * (kLaneRows * kSize) * p.ld_res);
-              }
 #pragma unroll
               for (int i = 0; i < kChunks / 32; ++i)
-                *reinterpret_cast<uint4*>(box + chunk(l_row + i * kLaneRows, l_chunk)) = v[i];
+                *reinterpret_cast<uint4*>(box + chunk(l_row + i * kLaneRows, l_chunk)) = res[i];
+              if (steps >> (s0 + kRows / 16) & 1u) load_residual(tb + kRows);
               __syncwarp();
             }
             if constexpr (!kF32) {
@@ -888,22 +901,16 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
             if constexpr (kRes && kF32) {
               // fp32 rows are whole 128-byte lines: the lanes add the residual and store them themselves (there are no
               // registers for a residual in the fragments' order beside the accumulator)
-              const float* src = static_cast<const float*>(p.residual) + (q.row0 + tb + l_row) * p.ld_res + l_col;
               float* dst = static_cast<float*>(p.D) + (q.row0 + tb + l_row) * p.ld_d + l_col;
-              float4 v[kChunks / 32];
-#pragma unroll
-              for (int i = 0; i < kChunks / 32; ++i) {
-                v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
-                  v[i] = *reinterpret_cast<const float4*>(src + i * kLaneRows * p.ld_res);
-              }
+              load_residual(tb);
               __syncwarp();
 #pragma unroll
               for (int i = 0; i < kChunks / 32; ++i) {
                 const float4 d = *reinterpret_cast<const float4*>(box + chunk(l_row + i * kLaneRows, l_chunk));
                 if (l_ok && tb + l_row + i * kLaneRows < q.cnt)
                   __stcs(reinterpret_cast<float4*>(dst + i * kLaneRows * p.ld_d),
-                         make_float4(d.x + v[i].x, d.y + v[i].y, d.z + v[i].z, d.w + v[i].w));
+                         make_float4(d.x + __uint_as_float(res[i].x), d.y + __uint_as_float(res[i].y),
+                                     d.z + __uint_as_float(res[i].z), d.w + __uint_as_float(res[i].w)));
               }
               __syncwarp();  // the box has been read
             } else if (tb + kRows <= q.cnt) {
@@ -1107,25 +1114,27 @@ bool choose_tile(const DeviceInfo& dev, FusedParams& p, int64_t num_kb) {
 }
 
 template <int KIND>
-int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8_t* sfB, const int32_t* offsets,
-              int64_t E, int64_t M, int64_t N, int64_t K, const float* alpha, const float* row_scale,
-              const uint16_t* bias, int act, int gated, const void* residual, int64_t ld_res, void* D, int d_dtype,
-              int64_t ld_d, cudaStream_t stream) {
-  const int64_t group = KIND == kNVF4 ? 16 : 32;
-  if (E < 1 || E > kMaxExperts || M < 0 || N < 0 || K <= 0 || K % 32 != 0) return BSP_ERR_INVALID_ARG;
-  if (d_dtype != BSP_OUT_BF16 && d_dtype != BSP_OUT_F32) return BSP_ERR_INVALID_ARG;
-  if (act < BSP_ACT_NONE || act > BSP_ACT_SILU || (gated != 0 && gated != 1)) return BSP_ERR_INVALID_ARG;
+int run_fused(const bsp_fused_gemm_desc* d, cudaStream_t stream) {
+  if (d == nullptr) return BSP_ERR_INVALID_ARG;
+  const int64_t group = KIND == kNVF4 ? 16 : 32, E = d->E, M = d->M, N = d->N, K = d->K;
+  if (E < 1 || E > (d->offsets ? kMaxExperts : 1) || M < 0 || N < 0 || K <= 0 || K % 32 != 0)
+    return BSP_ERR_INVALID_ARG;
+  if (d->d_dtype != BSP_OUT_BF16 && d->d_dtype != BSP_OUT_F32) return BSP_ERR_INVALID_ARG;
+  if (d->activation < BSP_ACT_NONE || d->activation > BSP_ACT_SILU || (d->gated != 0 && d->gated != 1))
+    return BSP_ERR_INVALID_ARG;
+  if ((d->offsets && d->residual) || (KIND == kMXF8 && d->row_scale)) return BSP_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return BSP_OK;
-  const int64_t cols = gated ? N / 2 : N;
-  if (N % (gated ? 16 : 8) != 0 || ld_d < cols || (residual && ld_res < cols)) return BSP_ERR_INVALID_ARG;
+  const int64_t cols = d->gated ? N / 2 : N;
+  if (N % (d->gated ? 16 : 8) != 0 || d->ld_d < cols || (d->residual && d->ld_residual < cols))
+    return BSP_ERR_INVALID_ARG;
   if (M > (1ll << 30) || N > (1ll << 30) || K > (1ll << 30)) return BSP_ERR_INVALID_ARG;
-  if (!A || !B || !sfA || !sfB || !D) return BSP_ERR_INVALID_ARG;
-  const int64_t esize = d_dtype == BSP_OUT_F32 ? 4 : 2;
-  if (!aligned16(A) || !aligned16(B) || !aligned16(sfA) || !aligned16(sfB) || !aligned16(D) ||
-      (bias && !aligned16(bias)) || (ld_d * esize) % 16 != 0 ||
-      (residual && (!aligned16(residual) || (ld_res * esize) % 16 != 0)) ||
-      ((reinterpret_cast<uintptr_t>(row_scale) | reinterpret_cast<uintptr_t>(alpha) |
-        reinterpret_cast<uintptr_t>(offsets)) & 3u))
+  if (!d->A || !d->B || !d->sfA || !d->sfB || !d->D) return BSP_ERR_INVALID_ARG;
+  const int64_t esize = d->d_dtype == BSP_OUT_F32 ? 4 : 2;
+  if (!aligned16(d->A) || !aligned16(d->B) || !aligned16(d->sfA) || !aligned16(d->sfB) || !aligned16(d->D) ||
+      (d->bias && !aligned16(d->bias)) || (d->ld_d * esize) % 16 != 0 ||
+      (d->residual && (!aligned16(d->residual) || (d->ld_residual * esize) % 16 != 0)) ||
+      ((reinterpret_cast<uintptr_t>(d->row_scale) | reinterpret_cast<uintptr_t>(d->alpha) |
+        reinterpret_cast<uintptr_t>(d->offsets)) & 3u))
     return BSP_ERR_ALIGNMENT;
   DeviceInfo dev;
   int st = current_device(&dev);
@@ -1133,25 +1142,25 @@ int run_fused(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint
   if (encode_tiled_fn() == nullptr) return BSP_ERR_CUDA;
 
   FusedArgs a;
-  a.A = A, a.sfA = sfA, a.B = B, a.sfB = sfB;
+  a.A = d->A, a.sfA = d->sfA, a.B = d->B, a.sfB = d->sfB;
   a.row_bytes = KIND == kNVF4 ? K / 2 : K;
   a.tiles_per_band = round_up(K / group, 4) / 4;
   FusedParams p = {};
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.E = static_cast<int>(E);
-  p.act = act;
-  p.gated = gated;
-  p.offsets = offsets;
-  p.alpha = alpha;
-  p.row_scale = row_scale;
-  p.bias = bias;
-  p.residual = residual;
-  p.ld_res = ld_res;
-  p.D = D;
-  p.ld_d = ld_d;
+  p.act = static_cast<int>(d->activation);
+  p.gated = static_cast<int>(d->gated);
+  p.offsets = d->offsets;
+  p.alpha = d->alpha;
+  p.row_scale = d->row_scale;
+  p.bias = d->bias;
+  p.residual = d->residual;
+  p.ld_res = d->ld_residual;
+  p.D = d->D;
+  p.ld_d = d->ld_d;
   p.err = dev.err_word;
-  const bool f32 = d_dtype == BSP_OUT_F32;
+  const bool f32 = d->d_dtype == BSP_OUT_F32;
   const bool pairs = choose_tile(dev, p, ceil_div(a.row_bytes, 128));
   return pairs ? launch_fused<KIND, 2>(dev, a, p, f32, stream) : launch_fused<KIND, 1>(dev, a, p, f32, stream);
 }

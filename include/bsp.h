@@ -438,58 +438,56 @@ int mxfp8_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uin
                const uint16_t *bias, void *D, int d_dtype, int64_t ld_d, bsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * GEMMs with a fused epilogue: a linear layer's activation (and the product
- * of a gated pair of projections) and the residual it is added to, in one
- * launch with the GEMM.
- *   y[m, n] = alpha * row_scale[m] * sum_k A(m,k) sA B(n,k) sB + bias[n]
+ * GEMMs with a fused epilogue, dense or grouped by expert: a linear layer's
+ * activation (and the product of a gated pair of projections) and the residual
+ * it is added to, or every expert's weight times its own rows of A, in one
+ * launch.  For e = 0 and every row m (offsets NULL), or for each expert e and
+ * offsets[e] <= m < offsets[e+1]:
+ *   y[m, n] = alpha[e] * row_scale[m] * sum_k A(m,k) sA B[e](n,k) sB[e] + bias[e, n]
  *   gated == 0: D[m, n] = act(y[m, n]) + residual[m, n]
  *   gated == 1: D[m, j] = act(y[m, 2j]) * y[m, 2j+1] + residual[m, j]
- * All of it in fp32, rounded once to the output type.
- *   A, sfA, B, sfB, alpha, row_scale, bias, D, d_dtype: as nvfp4_gemm /
- *              mxfp8_gemm.  gated: B's rows (and bias) alternate between the
- *              gate and the up projection, D has N/2 columns
- *   activation: BSP_ACT_*
- *   residual : [M, N or N/2] of D's element type, row stride ld_residual, or
- *              NULL.  It may be D itself (same pointer and stride); otherwise
- *              the two do not overlap.
- * Errors as nvfp4_gemm; an unknown activation, gated not 0 or 1, gated with
- * N % 16 != 0, or ld_residual below the columns of D -> INVALID_ARG;
- * a residual or ld_residual off 16 bytes -> ALIGNMENT. */
-int nvfp4_gemm_fused(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
-                     int64_t M, int64_t N, int64_t K, const float *alpha, const float *row_scale,
-                     const uint16_t *bias, int activation, int gated, const void *residual,
-                     int64_t ld_residual, void *D, int d_dtype, int64_t ld_d, bsp_stream_t stream);
-int mxfp8_gemm_fused(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
-                     int64_t M, int64_t N, int64_t K, const float *alpha, const uint16_t *bias,
-                     int activation, int gated, const void *residual, int64_t ld_residual, void *D,
-                     int d_dtype, int64_t ld_d, bsp_stream_t stream);
+ * All of it in fp32, rounded once to the output type.  Rows outside every
+ * expert are left as they were.
+ * The descriptor is HOST memory, read before the call returns; its pointers are
+ * device pointers.
+ *   A, sfA    : what the quantizers write for the whole [M, K] activation (128x4
+ *               scale tiles); grouped, the experts' tokens one expert after
+ *               another without padding
+ *   B         : codes [E, N, K/2] (NVFP4) or [E, N, K] (MXFP8), dense.  gated:
+ *               the rows (and the bias) alternate between the gate and the up
+ *               projection, D has N/2 columns
+ *   sfB       : E scale buffers of bsp_nvfp4_sf_bytes(N, K) /
+ *               bsp_mxfp8_sf_bytes(N, K) bytes one after another
+ *   offsets   : int32 [E + 1] or NULL (E = 1).  Values outside [0, M] are
+ *               clamped, and one below an earlier one counts as that one.  An
+ *               expert may have no row.
+ *   alpha     : fp32 [E] or NULL (1)
+ *   row_scale : fp32 [M] or NULL; NULL for MXFP8
+ *   bias      : bf16 [E, N] or NULL
+ *   residual  : [M, N or N/2] of D's element type, row stride ld_residual, or
+ *               NULL; NULL when grouped.  It may be D itself (same pointer and
+ *               stride); otherwise the two do not overlap.
+ *   D, d_dtype, ld_d : as nvfp4_gemm
+ * Errors as nvfp4_gemm; no descriptor, E outside 1 .. BSP_MAX_EXPERTS (without
+ * offsets: other than 1), an unknown activation, gated not 0 or 1, gated with
+ * N % 16 != 0, a row_scale or residual where there is none, or ld_residual below
+ * the columns of D -> INVALID_ARG; a residual or ld_residual off 16 bytes, or
+ * offsets off 4 -> ALIGNMENT. */
+typedef struct {
+    const uint8_t *A, *sfA, *B, *sfB;
+    const int32_t *offsets;
+    int64_t E, M, N, K;
+    const float *alpha, *row_scale;
+    const uint16_t *bias;
+    int64_t activation, gated; /* BSP_ACT_*, 0 or 1 */
+    const void *residual;
+    int64_t ld_residual;
+    void *D;
+    int64_t d_dtype, ld_d;
+} bsp_fused_gemm_desc;
 
-/* ------------------------------------------------------------------------
- * GEMMs grouped by expert: each expert's weight times its own rows of A, every
- * expert in one launch.  The rows of A are the experts' tokens one expert after
- * another, without padding; A and sfA are what the quantizers write for the
- * whole [M, K] activation.  For each expert e and offsets[e] <= m < offsets[e+1]:
- *   y[m, n] = alpha[e] * row_scale[m] * sum_k A(m,k) sA B[e](n,k) sB[e] + bias[e, n]
- * and D from y as in the fused epilogue above (no residual).  Rows outside
- * every expert are left as they were.
- *   B       : codes [E, N, K/2] (NVFP4) or [E, N, K] (MXFP8), dense
- *   sfB     : E scale buffers of bsp_nvfp4_sf_bytes(N, K) / bsp_mxfp8_sf_bytes(N, K)
- *             bytes one after another (each expert quantized by itself)
- *   offsets : int32 [E + 1] on the device.  Values outside [0, M] are clamped,
- *             and one below an earlier one counts as that one.  An expert may
- *             have no row.
- *   alpha   : fp32 [E] or NULL (1);  row_scale : fp32 [M] or NULL
- *   bias    : bf16 [E, N] or NULL
- * Errors as above; E outside 1 .. BSP_MAX_EXPERTS, or no offsets -> INVALID_ARG. */
-int nvfp4_grouped_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
-                       const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
-                       const float *alpha, const float *row_scale, const uint16_t *bias,
-                       int activation, int gated, void *D, int d_dtype, int64_t ld_d,
-                       bsp_stream_t stream);
-int mxfp8_grouped_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uint8_t *sfB,
-                       const int32_t *offsets, int64_t E, int64_t M, int64_t N, int64_t K,
-                       const float *alpha, const uint16_t *bias, int activation, int gated, void *D,
-                       int d_dtype, int64_t ld_d, bsp_stream_t stream);
+int nvfp4_gemm_fused(const bsp_fused_gemm_desc *desc, bsp_stream_t stream);
+int mxfp8_gemm_fused(const bsp_fused_gemm_desc *desc, bsp_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Device error word.

@@ -453,3 +453,112 @@ def test_refusals():
         bsp.nvfp4_gemm(a, bsp.NVFP4Tensor(B.codes[0][:24].contiguous(), B.sf[0], 64), gated=True)
     assert bsp.device_status() == 0
     assert down(res).any() == False  # noqa: E712
+
+
+# --------------------------------------------------------------------------- what callers do besides
+def test_operands_on_one_row_with_any_stride():
+    """A single row has no stride: out and residual from a broadcast or a slice."""
+    rng = np.random.default_rng(20)
+    A, B = Operand(rng, True, 1, 1, 64), Operand(rng, True, 1, 32, 64)
+    want = bsp.nvfp4_gemm(A.tensor(), B.tensor(), activation="silu", residual=torch.ones(1, 32, dtype=torch.bfloat16, device=DEV))
+    res = torch.ones(40, dtype=torch.bfloat16, device=DEV)[:32].expand(1, 32)
+    out = torch.empty(33, 8, 40, dtype=torch.bfloat16, device=DEV)[5, 3, :32].as_strided((1, 32), (7, 1))
+    assert torch.equal(want, bsp.nvfp4_gemm(A.tensor(), B.tensor(), activation="silu", residual=res, out=out))
+
+
+@pytest.mark.parametrize("M", [16, 100, 300])
+def test_infinite_and_nan_inputs_stay_in_their_rows(M):
+    """alpha, row scales, bias and residual that are infinite or NaN reach only the outputs that the formula gives them;
+    padding rows and columns hold nothing that leaks."""
+    rng = np.random.default_rng(M)
+    A, B = Operand(rng, True, 1, M, 128), Operand(rng, True, 1, 264, 128)
+    rs = torch.ones(M, device=DEV)
+    rs[3], rs[M - 1] = float("inf"), float("nan")
+    bias = torch.zeros(264, dtype=torch.bfloat16, device=DEV)
+    bias[5] = float("nan")
+    res = torch.zeros(M, 264, dtype=torch.bfloat16, device=DEV)
+    res[7, 9] = float("-inf")
+    got = bsp.nvfp4_gemm(A.tensor(), B.tensor(), None, rs, bias, activation="relu", residual=res)
+    plain = bsp.nvfp4_gemm(A.tensor(), B.tensor(), None, rs, bias, out_dtype=torch.float32)
+    # torch's clamp keeps NaN as the kernel does
+    want = plain.clamp(min=0) + res.float()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(torch.isinf(got), torch.isinf(want))
+    clean = torch.isfinite(want)
+    assert int((~clean).sum()) == int(torch.isnan(want).sum()) + int(torch.isinf(want).sum()) > 264
+    assert bool(((got.float() - want)[clean].abs() <= 2 ** -8 * want[clean].abs() + 1e-4).all())
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activation_tails(act):
+    """y far out on both sides, through the bias: relative accuracy down to each form's clamp, and the limits."""
+    vals = torch.tensor([-1e30, -1000, -60, -39, -20, -13, -9, -6.9, -5, -3, -1, -0.1, -1e-3, 0, 1e-3, 0.1, 1, 3, 5, 9, 20, 60, 1000,
+                         1e30], dtype=torch.float64)
+    rng = np.random.default_rng(21)
+    A, B = Operand(rng, True, 1, 2, 32), Operand(rng, True, 1, 24, 32)
+    zero = torch.zeros(1, device=DEV)
+    bias = vals.to(torch.bfloat16).to(DEV)
+    got = bsp.nvfp4_gemm(A.tensor(), B.tensor(), zero, None, bias, out_dtype=torch.float32, activation=act)[0].double().cpu().numpy()
+    y = bias.double().cpu().numpy()
+    want, rel = act64(y, act)
+    # below the clamp (silu -40, gelu_tanh -7) the value stays at the clamp's: 1.7e-16, 2.3e-15; gelu underflows past 13
+    floor = {"silu": 2e-16, "gelu_tanh": 3e-15, "gelu": 1e-37}[act]
+    tol = rel * np.abs(want) + 2 * U32 * np.maximum(y, 0) + 6e-7 * np.maximum(y, 0) * (act == "gelu") + floor
+    assert np.all(np.abs(got - want) <= tol), list(zip(y, got, want))
+
+
+def test_two_graphs_at_once():
+    """Two captured graphs of the same layer replayed on two streams at a time: nothing is shared between launches."""
+    rng = np.random.default_rng(22)
+    A, B = Operand(rng, True, 1, 64, 4608), Operand(rng, True, 1, 256, 4608)  # split over a cluster
+    C, D = Operand(rng, True, 1, 700, 256), Operand(rng, True, 5, 256, 256)
+    off = torch.tensor([0, 100, 100, 350, 699, 700], dtype=torch.int32, device=DEV)
+    run = lambda: (bsp.nvfp4_gemm(A.tensor(), B.tensor(), activation="gelu"),  # noqa: E731
+                   bsp.nvfp4_grouped_gemm(C.tensor(), D.experts(), off, activation="silu"))
+    want = run()
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in streams:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        graphs.append(g)
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, o) for pair in outs for w, o in zip(want, pair))
+    assert bsp.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 256, 8192), (40, 136, 13824), (128, 128, 4352), (1, 640, 9216)])
+def test_split_over_a_cluster(M, N, K):
+    """K shared by the CTAs of a cluster (few weight panels, long K): against the definition, and the same bits again."""
+    dense(np.random.default_rng(K), True, M, N, K, "silu", False, True, True, True)
+    dense(np.random.default_rng(K), False, M, N, K // 2, None, N % 16 == 0, True, False, False, torch.float32)
+    rng = np.random.default_rng(M)
+    A, B = Operand(rng, True, 1, M, K), Operand(rng, True, 1, N, K)
+    first = bsp.nvfp4_gemm(A.tensor(), B.tensor(), activation="relu")
+    for _ in range(30):
+        assert torch.equal(first, bsp.nvfp4_gemm(A.tensor(), B.tensor(), activation="relu"))
+
+
+def test_more_tiles_than_a_block_lists():
+    """A CTA's tiles past the ones it looks up first: many tiles of one small panel, dense and grouped."""
+    rng = np.random.default_rng(23)
+    A, B = Operand(rng, False, 1, 40000, 32), Operand(rng, False, 1, 512, 32)
+    alpha = torch.tensor([0.1], device=DEV)
+    got = bsp.mxfp8_gemm(A.tensor(), B.tensor(), alpha, activation="relu")
+    want = bsp.mxfp8_gemm(A.tensor(), B.tensor(), alpha, out_dtype=torch.float32).clamp(min=0)
+    assert bool(((got.float() - want).abs() <= 2 ** -8 * want + 1e-5).all())
+    counts = rng.integers(0, 40, size=512)
+    E, M = Operand(rng, False, 512, 2560, 32), int(counts.sum())
+    off = torch.from_numpy(np.concatenate(([0], np.cumsum(counts))).astype(np.int32)).to(DEV)
+    X = Operand(rng, False, 1, M, 32)
+    got = bsp.mxfp8_grouped_gemm(X.tensor(), E.experts(), off)
+    for e in (0, 1, 255, 300, 510, 511):
+        i, j = int(off[e]), int(off[e + 1])
+        if i < j:
+            ref, tol = reference(X.dec[0][i:j], E.dec[e], False, 1.0, None, None, None, False, None, torch.bfloat16)
+            check(got[i:j], ref, tol, f"expert {e}")
+    assert bsp.device_status() == 0
