@@ -435,12 +435,8 @@ def _activation_code(activation: str | None) -> int:
     return ACTIVATIONS[activation]
 
 
+_U8, _F32, _BF16 = torch.uint8, torch.float32, torch.bfloat16
 _OUT_CODES = {torch.bfloat16: nat.BSP_OUT_BF16, torch.float32: nat.BSP_OUT_F32}
-
-
-def _check_vector(name: str, t: torch.Tensor, dtype: torch.dtype, numel: int) -> None:
-    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {numel} elements")
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -480,14 +476,14 @@ def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, act
     else:
         E, N = shape[0], shape[1]
         ok = shape == (E, N, width)
-    if not (ok and cb.dtype is torch.uint8 and cb.is_contiguous()):
+    if not (ok and cb.dtype is _U8 and cb.is_contiguous()):
         raise ValueError(f"B: expected contiguous uint8 codes {'[N, ' if offsets is None else '[E, N, '}{width}], "
                          f"got {tuple(shape)}")
-    if ca.shape != (M, width) or ca.dtype is not torch.uint8 or not ca.is_contiguous():
+    if ca.shape != (M, width) or ca.dtype is not _U8 or not ca.is_contiguous():
         raise ValueError(f"A: expected contiguous uint8 codes [M, {width}], got {tuple(ca.shape)}")
-    if sfa.numel() != (M + 127) // 128 * tiles or sfa.dtype is not torch.uint8 or not sfa.is_contiguous():
+    if sfa.numel() != (M + 127) // 128 * tiles or sfa.dtype is not _U8 or not sfa.is_contiguous():
         raise ValueError(f"A: expected {(M + 127) // 128 * tiles} contiguous scale bytes, got {sfa.numel()}")
-    if sfb.numel() != E * ((N + 127) // 128) * tiles or sfb.dtype is not torch.uint8 or not sfb.is_contiguous():
+    if sfb.numel() != E * ((N + 127) // 128) * tiles or sfb.dtype is not _U8 or not sfb.is_contiguous():
         raise ValueError(f"B: expected {E * ((N + 127) // 128) * tiles} contiguous scale bytes, got {sfb.numel()}")
     cols = N
     if gated:
@@ -503,16 +499,23 @@ def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, act
     same = index == cb.get_device() == sfa.get_device() == sfb.get_device() == out.get_device() and index >= 0
     pal = prs = pbi = pre = pof = ld_res = 0  # 0: NULL
     if alpha is not None:
-        _check_vector("alpha", alpha, torch.float32, E)
-        same, pal = same and alpha.get_device() == index, alpha.data_ptr()
+        if alpha.dtype is not _F32 or alpha.numel() != E or not alpha.is_contiguous():
+            raise ValueError(f"alpha must be a contiguous fp32 tensor of {E} elements")
+        pal = alpha.data_ptr()
+        same = same and alpha.get_device() == index
     if row_scale is not None:
-        _check_vector("row_scale", row_scale, torch.float32, M)
-        same, prs = same and row_scale.get_device() == index, row_scale.data_ptr()
+        if row_scale.dtype is not _F32 or row_scale.numel() != M or not row_scale.is_contiguous():
+            raise ValueError(f"row_scale must be a contiguous fp32 tensor of {M} elements")
+        prs = row_scale.data_ptr()
+        same = same and row_scale.get_device() == index
     if bias is not None:
-        _check_vector("bias", bias, torch.bfloat16, E * N)
-        same, pbi = same and bias.get_device() == index, bias.data_ptr()
+        if bias.dtype is not _BF16 or bias.numel() != E * N or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous bf16 tensor of {E * N} elements")
+        pbi = bias.data_ptr()
+        same = same and bias.get_device() == index
     if offsets is not None:
-        same, pof = same and offsets.get_device() == index, offsets.data_ptr()
+        pof = offsets.data_ptr()
+        same = same and offsets.get_device() == index
     if residual is not None:
         if residual.dtype is not out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
             raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
