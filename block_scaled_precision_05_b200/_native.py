@@ -40,8 +40,7 @@ class BspWeightDesc(ctypes.Structure):
     _fields_ = [("w", _vp), ("N", _i64), ("K", _i64), ("ld_w", _i64), ("amax", _vp), ("gs", _vp), ("inv_gs", _vp),
                 ("codes", _vp), ("sf", _vp)]
 
-# bsp_fused_gemm_desc of include/bsp.h, 19 fields of 8 bytes in its order (pointers as integers, 0 for NULL).  Packed
-# bytes: a call with 18 converted arguments takes 1.3 us longer.
+# bsp_fused_gemm_desc of include/bsp.h: 19 fields of 8 bytes in its order (pointers as integers, 0 for NULL)
 pack_fused_desc = struct.Struct("=19q").pack
 
 # name -> (restype, argtypes), one entry per function declared in include/bsp.h
@@ -110,6 +109,24 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+_fused_gemm = None
+
+
+def fused_gemm():
+    """The binding of the fused GEMMs (csrc/fused_binding.cpp); raises if it has not been built."""
+    global _fused_gemm
+    if _fused_gemm is None:
+        lib()
+        try:
+            from . import _fused_binding
+        except ImportError as e:
+            raise RuntimeError("_fused_binding.so is missing or was built for another torch: build it with "
+                               "`python -m block_scaled_precision_05_b200.csrc.build` (or __graft_entry__.build()). "
+                               f"There is no fallback implementation. ({e})") from e
+        _fused_gemm = _fused_binding.fused_gemm
+    return _fused_gemm
 
 
 def status_string(status: int) -> str:

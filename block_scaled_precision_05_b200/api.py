@@ -429,116 +429,32 @@ def interleave_gated(gate: torch.Tensor, up: torch.Tensor, dim: int = -2) -> tor
     return torch.stack((gate, up), dim=d + 1).flatten(d, d + 1)
 
 
-def _activation_code(activation: str | None) -> int:
+def _check_activation(activation: str | None) -> None:
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    return ACTIVATIONS[activation]
-
-
-_U8, _F32, _BF16 = torch.uint8, torch.float32, torch.bfloat16
-_OUT_CODES = {torch.bfloat16: nat.BSP_OUT_BF16, torch.float32: nat.BSP_OUT_F32}
-
-
-def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
-    """Whether two row-major matrices of one shape and type share an element."""
-    lo_a, lo_b, size = a.data_ptr(), b.data_ptr(), a.element_size()
-    span = lambda t: ((t.shape[0] - 1) * t.stride(0) + t.shape[1]) * size  # noqa: E731
-    if a.numel() == 0 or lo_a >= lo_b + span(b) or lo_b >= lo_a + span(a):
-        return False
-    if a.stride(0) != b.stride(0):
-        return True
-    gap, ld = (lo_b - lo_a) // size, a.stride(0)
-    return gap % ld < a.shape[1] or -gap % ld < a.shape[1]  # column ranges modulo the common row stride
 
 
 def _fused(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual):
-    """The GEMMs with a fused epilogue: dense (offsets None, b one weight) and grouped (b stacked).  One path for both,
-    kept short: the smallest calls take as long on the host as on the GPU."""
+    """The GEMMs with a fused epilogue: dense (offsets None, b one weight) and grouped (b stacked).  The tensors are
+    checked, the output allocated and the kernel launched in csrc/fused_binding.cpp."""
     act = ACTIVATIONS.get(activation, -1)
     if act < 0:
-        _activation_code(activation)
+        _check_activation(activation)
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError("output dtype must be bf16 or fp32")
+    if a.K != b.K:
+        raise ValueError("A and B disagree on K")
     if fp4:
-        ca, cb = a.codes, b.codes
         if a.sf_layout != "128x4" or (offsets is None and b.sf_layout != "128x4"):
             raise ValueError("a fused epilogue or a grouped GEMM needs scales in the 128x4 layout")
+        r = nat.fused_gemm()(True, a.codes, a.sf, b.codes, b.sf, a.K, offsets, alpha, row_scale, bias,
+                             out_dtype is torch.float32, out, act, gated, residual)
     else:
-        ca, cb = a.q, b.q
-    sfa, sfb, K = a.sf, b.sf, a.K
-    if K != b.K:
-        raise ValueError("A and B disagree on K")
-    # sizes; a hand-made operand whose buffers are smaller than they say would be read out of range
-    M = ca.shape[0]
-    width, tiles = (K >> 1, ((K >> 4) + 3) // 4 * 512) if fp4 else (K, ((K >> 5) + 3) // 4 * 512)
-    shape = cb.shape
-    if offsets is None:
-        E, N = 1, shape[0]
-        ok = shape == (N, width)
-    else:
-        E, N = shape[0], shape[1]
-        ok = shape == (E, N, width)
-    if not (ok and cb.dtype is _U8 and cb.is_contiguous()):
-        raise ValueError(f"B: expected contiguous uint8 codes {'[N, ' if offsets is None else '[E, N, '}{width}], "
-                         f"got {tuple(shape)}")
-    if ca.shape != (M, width) or ca.dtype is not _U8 or not ca.is_contiguous():
-        raise ValueError(f"A: expected contiguous uint8 codes [M, {width}], got {tuple(ca.shape)}")
-    if sfa.numel() != (M + 127) // 128 * tiles or sfa.dtype is not _U8 or not sfa.is_contiguous():
-        raise ValueError(f"A: expected {(M + 127) // 128 * tiles} contiguous scale bytes, got {sfa.numel()}")
-    if sfb.numel() != E * ((N + 127) // 128) * tiles or sfb.dtype is not _U8 or not sfb.is_contiguous():
-        raise ValueError(f"B: expected {E * ((N + 127) // 128) * tiles} contiguous scale bytes, got {sfb.numel()}")
-    cols = N
-    if gated:
-        if N % 2 != 0:
-            raise ValueError("a gated weight has an even number of rows")
-        cols = N // 2
-    if out is None and out_dtype in _OUT_CODES:
-        out = ca.new_empty((M, cols), dtype=out_dtype)
-    else:
-        out, _ = _out(M, cols, out_dtype, ca.device, out)
-    # the operands' device, whose current stream the launch goes to; the optional operands
-    index = ca.get_device()
-    same = index == cb.get_device() == sfa.get_device() == sfb.get_device() == out.get_device() and index >= 0
-    pal = prs = pbi = pre = pof = ld_res = 0  # 0: NULL
-    if alpha is not None:
-        if alpha.dtype is not _F32 or alpha.numel() != E or not alpha.is_contiguous():
-            raise ValueError(f"alpha must be a contiguous fp32 tensor of {E} elements")
-        pal = alpha.data_ptr()
-        same = same and alpha.get_device() == index
-    if row_scale is not None:
-        if row_scale.dtype is not _F32 or row_scale.numel() != M or not row_scale.is_contiguous():
-            raise ValueError(f"row_scale must be a contiguous fp32 tensor of {M} elements")
-        prs = row_scale.data_ptr()
-        same = same and row_scale.get_device() == index
-    if bias is not None:
-        if bias.dtype is not _BF16 or bias.numel() != E * N or not bias.is_contiguous():
-            raise ValueError(f"bias must be a contiguous bf16 tensor of {E * N} elements")
-        pbi = bias.data_ptr()
-        same = same and bias.get_device() == index
-    if offsets is not None:
-        pof = offsets.data_ptr()
-        same = same and offsets.get_device() == index
-    if residual is not None:
-        if residual.dtype is not out.dtype or residual.shape != out.shape or residual.stride(1) != 1:
-            raise ValueError(f"residual must be a row-major [{M}, {cols}] tensor of the output's dtype")
-        same, pre, ld_res = same and residual.get_device() == index, residual.data_ptr(), residual.stride(0)
-    pd, ld = out.data_ptr(), out.stride(0)
-    if M == 1:  # one row has no stride: a broadcast or sliced tensor's is anything
-        ld = ld_res = (cols + 7) // 8 * 8
-    if not same:
-        _require_cuda(ca, sfa, cb, sfb, offsets, alpha, row_scale, bias, residual, out)
-        raise ValueError("operands on different devices")
-    if pre and (pre != pd or ld_res != ld) and _overlap(residual, out):
-        raise ValueError("residual may be the output itself, but must not overlap it otherwise")
-    if index != torch._C._cuda_getDevice():
-        with torch.cuda.device(index):
-            return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, residual)
-
-    desc = nat.pack_fused_desc(ca.data_ptr(), sfa.data_ptr(), cb.data_ptr(), sfb.data_ptr(), pof, E, M, N, K, pal, prs,
-                               pbi, act, 1 if gated else 0, pre, ld_res, pd, _OUT_CODES[out.dtype], ld)
-    L = nat.lib()
-    st = (L.nvfp4_gemm_fused if fp4 else L.mxfp8_gemm_fused)(desc, _stream(index))
-    if st:
-        nat.check(st, "nvfp4_gemm_fused" if fp4 else "mxfp8_gemm_fused")
-    return out
+        r = nat.fused_gemm()(False, a.q, a.sf, b.q, b.sf, a.K, offsets, alpha, None, bias, out_dtype is torch.float32, out,
+                             act, gated, residual)
+    if type(r) is int:
+        nat.check(r, "nvfp4_gemm_fused" if fp4 else "mxfp8_gemm_fused")
+    return r
 
 
 def nvfp4_gemm(a: NVFP4Tensor, b: NVFP4Tensor, alpha: torch.Tensor | None = None,
@@ -665,15 +581,6 @@ def mxfp8_quantize_experts(w: torch.Tensor) -> MXFP8Experts:
     return q
 
 
-def _grouped_gemm(fp4: bool, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated):
-    E = (b.codes if fp4 else b.q).shape[0]
-    if not 1 <= E <= nat.BSP_MAX_EXPERTS:
-        raise ValueError(f"1 to {nat.BSP_MAX_EXPERTS} experts, got {E}")
-    if offsets is None or offsets.dtype is not torch.int32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must be a contiguous int32 tensor of {E + 1} elements")
-    return _fused(fp4, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, None)
-
-
 def nvfp4_grouped_gemm(a: NVFP4Tensor, b: NVFP4Experts, offsets: torch.Tensor, alpha: torch.Tensor | None = None,
                        row_scale: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
@@ -687,7 +594,9 @@ def nvfp4_grouped_gemm(a: NVFP4Tensor, b: NVFP4Experts, offsets: torch.Tensor, a
     [M, K] activation; offsets int32 [E + 1] on the device; alpha fp32 [E], bias
     bf16 [E, N].  Rows outside every expert keep what `out` held (without `out`
     they are undefined)."""
-    return _grouped_gemm(True, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated)
+    if offsets is None:
+        raise ValueError("offsets must be an int32 tensor")
+    return _fused(True, a, b, offsets, alpha, row_scale, bias, out_dtype, out, activation, gated, None)
 
 
 def mxfp8_grouped_gemm(a: MXFP8Tensor, b: MXFP8Experts, offsets: torch.Tensor, alpha: torch.Tensor | None = None,
@@ -695,7 +604,9 @@ def mxfp8_grouped_gemm(a: MXFP8Tensor, b: MXFP8Experts, offsets: torch.Tensor, a
                        out: torch.Tensor | None = None, activation: str | None = None,
                        gated: bool = False) -> torch.Tensor:
     """nvfp4_grouped_gemm for MXFP8 operands."""
-    return _grouped_gemm(False, a, b, offsets, alpha, None, bias, out_dtype, out, activation, gated)
+    if offsets is None:
+        raise ValueError("offsets must be an int32 tensor")
+    return _fused(False, a, b, offsets, alpha, None, bias, out_dtype, out, activation, gated, None)
 
 
 def device_status() -> int:
@@ -822,7 +733,7 @@ class NVFP4GroupedLinear:
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, per_token: bool = False,
                  four_over_six: bool = False, activation: str | None = None, gated: bool = False):
-        _activation_code(activation)
+        _check_activation(activation)
         self.weight, self.gs_w, self.inv_gs_w = nvfp4_quantize_experts(
             weight, FP8_FP4_MAX_4OVER6 if four_over_six else FP8_FP4_MAX)
         self.experts, self.in_features = weight.shape[0], weight.shape[2]
@@ -849,7 +760,7 @@ class MXFP8GroupedLinear:
 
     def __init__(self, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
                  gated: bool = False):
-        _activation_code(activation)
+        _check_activation(activation)
         self.weight = mxfp8_quantize_experts(weight)
         self.experts, self.in_features = weight.shape[0], weight.shape[2]
         self.out_features = weight.shape[1] // 2 if gated else weight.shape[1]

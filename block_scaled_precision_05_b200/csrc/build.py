@@ -1,4 +1,5 @@
-"""Builds libbsp.so (the C-ABI CUDA library) in-tree for sm_100a.
+"""Builds libbsp.so (the C-ABI CUDA library) in-tree for sm_100a, and the
+CPython binding of its fused GEMMs (_fused_binding.so, plain C++ over it).
 
     python -m block_scaled_precision_05_b200.csrc.build [--force] [--verbose]
 
@@ -21,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
+BINDING = os.path.join(PKG, "_fused_binding.so")
 SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "fused_gemm_nvfp4.cu", "fused_gemm_mxfp8.cu"]
 HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "fused_gemm.cuh", "norm_stats.cuh", "tensor_maps.h"]
 
@@ -75,6 +77,31 @@ def _compile(src: str, verbose: bool, extra: list[str]) -> str:
     return obj
 
 
+def _build_binding(verbose: bool) -> None:
+    """csrc/fused_binding.cpp against torch's headers and libbsp.so (found next to it at run time)."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(HERE, "fused_binding.cpp")
+    if not _stale(BINDING, [src, os.path.join(INCLUDE, "bsp.h"), os.path.abspath(__file__)]):
+        return
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(cuda_lib_dir()), "include")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(top, "include"),
+           "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-I", cuda, src, "-o", tmp,
+           "-L", PKG, "-l:libbsp.so", "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fused_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every source for sm_100a and link libbsp.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -95,6 +122,9 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if force and os.path.exists(BINDING):
+        os.remove(BINDING)
+    _build_binding(verbose)
     return LIB
 
 

@@ -126,14 +126,3 @@ def test_interleave_gated():
     assert b.tolist() == [0, 10, 2, 12, 4, 14]
     with pytest.raises(ValueError):
         bsp.interleave_gated(g, u[:2])
-
-
-def test_overlap_of_strided_matrices():
-    buf = torch.zeros(64)
-    m = lambda off, ld, r, c: torch.as_strided(buf, (r, c), (ld, 1), off)  # noqa: E731
-    assert not api._overlap(m(0, 16, 4, 8), m(8, 16, 4, 8))  # two halves of one wide matrix
-    assert api._overlap(m(0, 16, 4, 8), m(7, 16, 4, 8))
-    assert api._overlap(m(8, 16, 3, 9), m(16, 16, 3, 9))
-    assert not api._overlap(m(0, 8, 4, 8), m(32, 8, 4, 8))
-    assert api._overlap(m(0, 8, 4, 8), m(24, 8, 4, 8))
-    assert api._overlap(m(0, 8, 4, 8), m(16, 10, 4, 8))  # other strides: refused where the ranges meet

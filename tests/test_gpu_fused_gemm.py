@@ -562,3 +562,20 @@ def test_more_tiles_than_a_block_lists():
             ref, tol = reference(X.dec[0][i:j], E.dec[e], False, 1.0, None, None, None, False, None, torch.bfloat16)
             check(got[i:j], ref, tol, f"expert {e}")
     assert bsp.device_status() == 0
+
+
+def test_overlapping_residuals_are_refused():
+    """A residual may be the output itself or share no element with it: halves of one wide matrix, rows apart."""
+    rng = np.random.default_rng(24)
+    A, B = Operand(rng, True, 1, 4, 64).tensor(), Operand(rng, True, 1, 8, 64).tensor()
+    buf = torch.zeros(128, dtype=torch.bfloat16, device=DEV)
+    m = lambda off, ld: torch.as_strided(buf, (4, 8), (ld, 1), off)  # noqa: E731
+    run = lambda out, res: bsp.nvfp4_gemm(A, B, out=out, residual=res)  # noqa: E731
+    for out, res in ((m(0, 16), m(8, 16)), (m(8, 16), m(0, 16)), (m(0, 8), m(32, 8)), (m(0, 16), m(0, 16)), (m(0, 24), m(8, 24)),
+                     (m(0, 24), m(16, 24)), (m(8, 16), m(16, 16))):
+        buf.zero_()
+        want = bsp.nvfp4_gemm(A, B, activation=None, residual=torch.zeros(4, 8, dtype=torch.bfloat16, device=DEV))
+        assert torch.equal(run(out, res), want)
+    for out, res in ((m(0, 8), m(24, 8)), (m(0, 8), m(16, 16)), (m(0, 16), m(0, 8)), (m(0, 16), m(0, 24))):
+        with pytest.raises(ValueError, match="overlap"):
+            run(out, res)
