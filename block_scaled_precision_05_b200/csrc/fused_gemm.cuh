@@ -1100,12 +1100,15 @@ int launch_fused(const DeviceInfo& dev, const FusedArgs& a, const FusedParams& p
 //    18.2 / 20.5), but its epilogue and its larger tiles take longer where everything runs at once (M = 256, N = 5120,
 //    K = 13824: 28.6 / 23.0).  Up to 8 K steps the single form's second accumulator, which overlaps the epilogue with
 //    the next tile, is worth up to three waves (M = 4096, N = K = 1536: 16.4 / 14.2).
-//    Experts: single up to a mean of 64 rows (128 experts of 1536 x 2048: 50.4 / 53.1 at 64 rows, 60.5 / 71.7 at 128;
-//    8 of 13824 x 5120: 60.9 / 58.3 and 66.3 / 78.9).
+//    Experts: single up to a mean of 64 rows (with up to 4 K steps: 160), and above it while about 3.5 waves of single
+//    tiles hold them all (us, pairs / single: 128 experts of 1536 x 2048 at 64 rows 48.1 / 48.0, at 128 56.5 / 62.4;
+//    128 of 2048 x 768 at 128 rows 47.3 / 44.3; 16 of 2048 x 2048 at 128 rows, 2.6 waves, 20.1 / 16.5, at 256 20.9 /
+//    22.7; 8 of 5120 x 5120 at 128 rows, 3.2 waves, 32.3 / 31.0, at 192 35.5 / 42.2).
 //  - Single CTAs, token tile 32, 64 or 128: narrow tiles leave room for a deeper ring, but cost a pass over the weight
 //    each.  Dense: the smallest that covers M; with up to 8 K steps, where a tile's time is its epilogue's, the
 //    smallest whose tiles fit in one wave (M = 256, N = K = 1536: 6.9 against 7.4 at 128).  Experts: 32 up to a mean
-//    of 8 rows, 64 up to 16 (128 experts: 39.9 / 40.6 / 41.4 at 8 rows, 47.1 / 42.8 / 43.8 at 16).
+//    of 8 rows, 64 up to 24 (128 experts of 1536 x 2048, tiles of 32 / 64 / 128: 39.9 / 40.6 / 41.4 at 8 rows, 41.8 /
+//    39.7 / 40.9 at 16, 53.1 / 43.3 / 41.1 at 32).
 bool choose_tile(const DeviceInfo& dev, FusedParams& p, int64_t num_kb) {
   const int64_t panels = ceil_div(p.N, 128), waves = num_kb <= 8 ? 3 : 1;
   if (p.offsets == nullptr) {
@@ -1118,11 +1121,12 @@ bool choose_tile(const DeviceInfo& dev, FusedParams& p, int64_t num_kb) {
     return false;
   }
   const int64_t rows = ceil_div(p.M, p.E);
-  if (rows > 64) {
+  const int64_t single = (2 * ceil_div(p.M, 128) + p.E) * panels;  // twice the single tiles, about
+  if (rows > (num_kb <= 4 ? 160 : 64) && single > 7 * dev.sm_count) {
     p.tn = 256;
     return true;
   }
-  p.tn = rows <= 8 ? 32 : rows <= 16 ? 64 : 128;
+  p.tn = rows <= 8 ? 32 : rows <= 24 ? 64 : 128;
   return false;
 }
 
