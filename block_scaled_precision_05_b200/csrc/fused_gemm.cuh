@@ -148,15 +148,6 @@ struct Table {
     lo = start + kMaxExperts + 1;
   }
 
-  __device__ __forceinline__ void build_dense(const FusedParams& p) {
-    if (threadIdx.x == 0) {
-      lo[0] = 0;
-      lo[1] = p.M;
-      start[0] = 0;
-      start[1] = (p.M + p.tn - 1) / p.tn * p.panels;
-    }
-  }
-
   // Offsets are clamped to [0, M], and one below an earlier one counts as that one, so that the experts' rows never
   // overlap whatever the array holds.  Called by the whole CTA.
   __device__ __forceinline__ void build(const FusedParams& p) {
@@ -197,21 +188,14 @@ struct Table {
     __syncthreads();
   }
 
-  // Tile t: its expert by bisection, then token tiles within groups of group_m, fastest first, so that the CTAs that
-  // run at once share weight panels and tokens in L2.  An expert's rows are shared out evenly over its tiles.
+  // Tile r of the expert e that has rows l .. l + rows - 1: token tiles within groups of group_m, fastest first, so
+  // that the CTAs that run at once share weight panels and tokens in L2.  The rows are shared out evenly over the tiles.
   template <int N_STEP>
-  __device__ __forceinline__ Tile get(int t, const FusedParams& p) const {
+  static __device__ __forceinline__ Tile locate(int e, int l, int rows, int r, const FusedParams& p) {
     const int TN = p.tn;
-    int a = 0, b = p.E;
-    while (b - a > 1) {
-      const int mid = (a + b) >> 1;
-      if (start[mid] <= t) a = mid;
-      else b = mid;
-    }
-    const int l = lo[a], rows = lo[a + 1] - l;
     const int nt = rows <= TN ? 1 : (rows + TN - 1) / TN;
-    int r = t - start[a], first = 0, size = nt, per = (rows + N_STEP - 1) / N_STEP * N_STEP;
-    if (nt > 1) {  // (divisions are slow, and every role waits for its first tile)
+    int first = 0, size = nt, per = (rows + N_STEP - 1) / N_STEP * N_STEP;
+    if (nt > 1) {  // (divisions are slow)
       per = ((rows + nt - 1) / nt + N_STEP - 1) / N_STEP * N_STEP;
       if (nt > p.group_m) {
         const int per_group = p.group_m * p.panels;
@@ -222,14 +206,26 @@ struct Table {
       }
     }
     const int nb = size > 1 ? r / size : r;
-    const int mt = first + r - nb * size;
     Tile q;
-    q.e = a;
+    q.e = e;
     q.nb = nb;
-    q.row0 = l + mt * per;
+    q.row0 = l + (first + r - nb * size) * per;
     q.cnt = min(per, l + rows - q.row0);
     q.nmma = (q.cnt + N_STEP - 1) / N_STEP * N_STEP;
     return q;
+  }
+
+  // Tile t: its expert by bisection.
+  template <int N_STEP>
+  __device__ __forceinline__ Tile get(int t, const FusedParams& p) const {
+    if (p.offsets == nullptr) return locate<N_STEP>(0, 0, p.M, t, p);
+    int a = 0, b = p.E;
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if (start[mid] <= t) a = mid;
+      else b = mid;
+    }
+    return locate<N_STEP>(a, lo[a], lo[a + 1] - lo[a], t - start[a], p);
   }
 };
 
@@ -337,27 +333,29 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   const int kb0 = k_split > 1 ? p.num_kb * k_rank / k_split : 0;
   const int kb1 = k_split > 1 ? p.num_kb * (k_rank + 1) / k_split : p.num_kb;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < n_stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-      mbar_init(&sf_ready[s], C::SF_WARPS + kPeerArrivals);
-      mbar_init(&sf_local[s], C::SF_WARPS);
+  if (warp == 0) {  // one lane a stage
+    if (static_cast<int>(lane) < n_stages) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&empty[lane], 1);
+      mbar_init(&sf_ready[lane], C::SF_WARPS + kPeerArrivals);
+      mbar_init(&sf_local[lane], C::SF_WARPS);
+    } else if (lane >= 16u && lane < 18u) {
+      mbar_init(&acc_full[lane - 16u], 1);
+      mbar_init(&acc_empty[lane - 16u], C::EPI_WARPS + kPeerArrivals);
+    } else if (lane == 18u) {
+      mbar_init(acc_local, C::EPI_WARPS);
+      mbar_init(drain, 1);
+      mbar_init(part_ready, static_cast<uint32_t>(k_split * C::EPI_WARPS));
+      *abort_flag = 0u;
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], C::EPI_WARPS + kPeerArrivals);
-    }
-    mbar_init(acc_local, C::EPI_WARPS);
-    mbar_init(drain, 1);
-    mbar_init(part_ready, static_cast<uint32_t>(k_split * C::EPI_WARPS));
-    *abort_flag = 0u;
     fence_barrier_init();
-    prefetch_tensormap(&maps.w);
-    prefetch_tensormap(&maps.sfw);
-    for (int i = 0; i < p.tn / (32 * C::CG); ++i) prefetch_tensormap(&maps.x[i]);
-    for (int i = 0; i < C::X_BANDS; ++i) prefetch_tensormap(&maps.sfx[i]);
-    prefetch_tensormap(&maps.d);
+  } else if (warp == 2) {
+    const int i = static_cast<int>(lane);
+    if (i == 0) prefetch_tensormap(&maps.w);
+    else if (i == 1) prefetch_tensormap(&maps.sfw);
+    else if (i == 2) prefetch_tensormap(&maps.d);
+    else if (i >= 4 && i - 4 < p.tn / (32 * C::CG)) prefetch_tensormap(&maps.x[i - 4]);
+    else if (i >= 8 && i - 8 < C::X_BANDS) prefetch_tensormap(&maps.sfx[i - 8]);
   }
   if (warp == 1) {
     if constexpr (C::CG == 2) {
@@ -369,7 +367,24 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
     }
   }
   __syncwarp();
-  if (p.offsets == nullptr) table.build_dense(p);
+  const int first_tile = static_cast<int>(blockIdx.x) / (C::CG * k_split);
+  const int tile_step = static_cast<int>(gridDim.x) / (C::CG * k_split);
+  // This CTA's first tiles are looked up once, side by side: a lookup takes 500 to 1000 clocks (a bisection and
+  // divisions, between instructions that have to be fetched again), and one in front of every tile of every role cost
+  // 2400 a tile in the epilogue (128 experts, 32768 x 2048 x 768: 72 us against 60).
+  auto list_tiles = [&](int tiles) {
+    const int i = static_cast<int>(threadIdx.x) - C::THREADS + kListed;  // the last warps: the first ones set up
+    const int64_t t = first_tile + static_cast<int64_t>(i) * tile_step;
+    if (i >= 0 && t < tiles) {
+      const Tile q = table.get<C::N_STEP>(static_cast<int>(t), p);
+      list[i] = make_int4(q.e, q.nb, q.row0, q.cnt);
+    }
+  };
+  int num_tiles = 0;
+  if (p.offsets == nullptr) {
+    num_tiles = (p.M + p.tn - 1) / p.tn * p.panels;
+    list_tiles(num_tiles);
+  }
   tc_fence_before_sync();
   __syncwarp();
   if (C::CG == 2 || k_split > 1)
@@ -379,23 +394,14 @@ __global__ void __launch_bounds__(FCfg<KIND, CG>::THREADS, 1)
   // Set-up above overlaps the previous kernel under programmatic launch; every global access below comes after its
   // completion.
   grid_dependency_wait();
-  if (p.offsets != nullptr) table.build(p);
+  if (p.offsets != nullptr) {
+    table.build(p);
+    num_tiles = table.start[p.E];
+    list_tiles(num_tiles);
+    __syncthreads();
+  }
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int num_tiles = table.start[p.E];
-  const int first_tile = static_cast<int>(blockIdx.x) / (C::CG * k_split);
-  const int tile_step = static_cast<int>(gridDim.x) / (C::CG * k_split);
-  // This CTA's first tiles are looked up once, side by side: a lookup takes 500 to 1000 clocks (a bisection and
-  // divisions, between instructions that have to be fetched again), and one in front of every tile of every role cost
-  // 2400 a tile in the epilogue (128 experts, 32768 x 2048 x 768: 72 us against 60).
-  if (threadIdx.x < kListed) {
-    const int64_t t = first_tile + static_cast<int64_t>(threadIdx.x) * tile_step;
-    if (t < num_tiles) {
-      const Tile q = table.get<C::N_STEP>(static_cast<int>(t), p);
-      list[threadIdx.x] = make_int4(q.e, q.nb, q.row0, q.cnt);
-    }
-  }
-  __syncthreads();
   auto tile_at = [&](int t, int it) {
     if (it >= kListed) return table.get<C::N_STEP>(t, p);
     const int4 v = list[it];
