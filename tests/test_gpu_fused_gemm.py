@@ -579,3 +579,42 @@ def test_overlapping_residuals_are_refused():
     for out, res in ((m(0, 8), m(24, 8)), (m(0, 8), m(16, 16)), (m(0, 16), m(0, 8)), (m(0, 16), m(0, 24))):
         with pytest.raises(ValueError, match="overlap"):
             run(out, res)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300, 1500])
+def test_dependent_launches_back_to_back(M):
+    """Each launch adds onto the output of the one before (residual in place), and every second one reads what a plain
+    GEMM and a quantizer just wrote: the same bits whether or not the host waits in between, eager and from a graph."""
+    rng = np.random.default_rng(M)
+    A, B = Operand(rng, True, 1, M, 512), Operand(rng, True, 1, 512, 512)
+    alpha = torch.tensor([0.02], device=DEV)
+    one = torch.ones(1, device=DEV)
+    a, b = A.tensor(), B.tensor()
+
+    def chain(wait):
+        x = torch.zeros(M, 512, dtype=torch.bfloat16, device=DEV)
+        q = a
+        for _ in range(6):
+            bsp.nvfp4_gemm(q, b, alpha, activation="silu", residual=x, out=x)
+            wait()
+            bsp.nvfp4_gemm(q, b, alpha, activation="relu", residual=x, out=x)
+            wait()
+            y = bsp.nvfp4_gemm(q, b, alpha, out_dtype=torch.bfloat16)
+            wait()
+            x2 = bsp.nvfp4_gemm(q, b, alpha, activation="gelu", residual=y)
+            wait()
+            q = bsp.nvfp4_quantize(x2, one)
+            wait()
+        return x
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(want, chain(lambda: None))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(want, got)
+    assert bsp.device_status() == 0
