@@ -34,9 +34,10 @@ __device__ __forceinline__ float max_nan(float x, float c) {
   return y;
 }
 
-// x / (1 + 2^e(x)) for both, e(x) <= 60 so that the product of the denominators stays in range.
+// x / (1 + 2^e(x)) for both, e(x) <= 60 so that the product of the denominators stays in range.  The minimum takes
+// nothing but a NaN, which must not reach the other value through the shared reciprocal: x itself keeps it.
 __device__ __forceinline__ void logistic2(float& x0, float& x1, float e0, float e1) {
-  const float p = 1.0f + ex2_approx(e0), q = 1.0f + ex2_approx(e1);
+  const float p = 1.0f + ex2_approx(fminf(e0, 60.0f)), q = 1.0f + ex2_approx(fminf(e1, 60.0f));
   const float r = rcp_approx(p * q);
   x0 *= r * q;
   x1 *= r * p;

@@ -618,3 +618,23 @@ def test_dependent_launches_back_to_back(M):
         torch.cuda.synchronize()
         assert torch.equal(want, got)
     assert bsp.device_status() == 0
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", [None, "relu", "gelu", "gelu_tanh", "silu"])
+def test_nan_stays_in_its_column(act, gated):
+    """One column that is NaN or infinite (through the bias) changes no bit of any other, though two share a reciprocal."""
+    rng = np.random.default_rng(33)
+    A, B = Operand(rng, True, 1, 40, 128), Operand(rng, True, 1, 256, 128)
+    plain = torch.zeros(256, dtype=torch.bfloat16, device=DEV)
+    want = bsp.nvfp4_gemm(A.tensor(), B.tensor(), None, None, plain, activation=act, gated=gated)
+    assert bool(torch.isfinite(want).all())
+    for col in (0, 21, 138, 255):
+        for value in ("nan", "inf", "-inf"):
+            bias = plain.clone()
+            bias[col] = float(value)
+            got = bsp.nvfp4_gemm(A.tensor(), B.tensor(), None, None, bias, activation=act, gated=gated)
+            at = col // 2 if gated else col
+            others = torch.arange(want.shape[1], device=DEV) != at
+            assert torch.equal(got[:, others], want[:, others]), (col, value)
+            assert value != "nan" or bool(torch.isnan(got[:, at]).all())
