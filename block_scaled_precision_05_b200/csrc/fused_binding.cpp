@@ -1,7 +1,7 @@
 // fused_binding.cpp -- the binding of the fused and grouped GEMMs: one CPython call that checks the tensors, allocates
 // the output and calls the C ABI.  The smallest of these GEMMs take 6 to 12 us on the GPU; the same checks written in
-// Python take 10.4 us a call, here 5.5 (2.5 of them the
-// launch and its tensor maps).  Everything else of the package is bound through ctypes.
+// Python take 10.4 us a call, here 5.5 (2.5 of them the launch and its tensor maps).  Everything else of the package is
+// bound through ctypes.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -46,6 +46,15 @@ bool overlap(const at::Tensor& a, const at::Tensor& b) {
   const int64_t gap = (((pb - pa) / size) % ld + ld) % ld;  // column ranges modulo the common row stride
   return gap < cols || (ld - gap) % ld < cols;
 }
+
+// Other Python threads run while this one allocates and launches (either may block: a full launch queue waits for the
+// stream, and a host function in the stream may wait for the interpreter).
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 struct Call {
   int64_t fp4, K, activation, gated;
@@ -124,30 +133,35 @@ PyObject* run(const Call& c) {
   if (!cuda) refuse("libbsp runs on CUDA tensors only (no CPU path)");
   if (!same) refuse("operands on different devices");
 
-  // the launch goes to the operands' device and its current stream
-  const c10::cuda::CUDAGuard guard(device);
-  const at::Tensor out = c.out != Py_None ? THPVariable_Unpack(c.out)
-                                          : at::empty({M, cols}, at::TensorOptions().dtype(type).device(device));
-  d.D = out.data_ptr();
-  d.ld_d = out.stride(0);
-  if (M == 1) d.ld_d = d.ld_residual = (cols + 7) / 8 * 8;  // one row has no stride: a broadcast's or a slice's is anything
-  if (d.residual != nullptr && (d.residual != d.D || d.ld_residual != d.ld_d)) {
-    if (overlap(THPVariable_Unpack(c.residual), out))
-      refuse("residual may be the output itself, but must not overlap it otherwise");
+  at::Tensor out;
+  int status;
+  {
+    const Unlocked unlocked;
+    // the launch goes to the operands' device and its current stream
+    const c10::cuda::CUDAGuard guard(device);
+    out = c.out != Py_None ? THPVariable_Unpack(c.out)
+                           : at::empty({M, cols}, at::TensorOptions().dtype(type).device(device));
+    d.D = out.data_ptr();
+    d.ld_d = out.stride(0);
+    if (M == 1) d.ld_d = d.ld_residual = (cols + 7) / 8 * 8;  // one row has no stride: a broadcast's or a slice's is anything
+    if (d.residual != nullptr && (d.residual != d.D || d.ld_residual != d.ld_d)) {
+      if (overlap(THPVariable_Unpack(c.residual), out))
+        refuse("residual may be the output itself, but must not overlap it otherwise");
+    }
+    d.A = static_cast<const uint8_t*>(ca.data_ptr());
+    d.sfA = static_cast<const uint8_t*>(sfa.data_ptr());
+    d.B = static_cast<const uint8_t*>(cb.data_ptr());
+    d.sfB = static_cast<const uint8_t*>(sfb.data_ptr());
+    d.E = E;
+    d.M = M;
+    d.N = N;
+    d.K = K;
+    d.activation = c.activation;
+    d.gated = c.gated;
+    d.d_dtype = f32 ? BSP_OUT_F32 : BSP_OUT_BF16;
+    const bsp_stream_t stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+    status = fp4 ? nvfp4_gemm_fused(&d, stream) : mxfp8_gemm_fused(&d, stream);
   }
-  d.A = static_cast<const uint8_t*>(ca.data_ptr());
-  d.sfA = static_cast<const uint8_t*>(sfa.data_ptr());
-  d.B = static_cast<const uint8_t*>(cb.data_ptr());
-  d.sfB = static_cast<const uint8_t*>(sfb.data_ptr());
-  d.E = E;
-  d.M = M;
-  d.N = N;
-  d.K = K;
-  d.activation = c.activation;
-  d.gated = c.gated;
-  d.d_dtype = f32 ? BSP_OUT_F32 : BSP_OUT_BF16;
-  const bsp_stream_t stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
-  const int status = fp4 ? nvfp4_gemm_fused(&d, stream) : mxfp8_gemm_fused(&d, stream);
   if (status != BSP_OK) return PyLong_FromLong(status);
   if (c.out != Py_None) {
     Py_INCREF(c.out);
