@@ -29,11 +29,13 @@
 //  - experts of a few hundred rows: per tile, the hand-over of the one 256-column accumulator (last MMA to first MMA of
 //    the next tile, about 3000 clocks) beside 8 K steps of 520 to 600 clocks: 128 experts, 32768 rows, 1536 x 2048 gated
 //    81 us.  Two 128-column accumulators instead (no hand-over, twice the weight traffic): 112 us.
-//  - short K: the epilogue, about 800 clocks per warp for 32 tokens x 32 columns (conversions, the turn through shared
-//    memory, the store), plus 8 to 12 clocks of the special-function unit for each activated value.
+//  - short K: the epilogue, about 900 clocks per warp for 32 tokens x 32 columns (200 of arithmetic, then one after
+//    another the buffer's wait, the turn through shared memory, the fence and the store), plus 8 to 12 clocks of the
+//    special-function unit for each activated value: 128 experts, 32768 x 2048 x 768 59 us, without it 43.
 //  - decoding batches: the weight stream; 512 rows over 117 of 128 experts of 1536 x 2048, 208 MB in 34.4 us, 6.05 TB/s.
 // Not kept: an L2 prefetch of the next tile's weights (3 to 12% slower); the follower's warps arriving on the leader's
-// barriers themselves (2 to 10% slower); experts dealt out in the order of their tiles' widths (1 to 2% slower).
+// barriers themselves (2 to 10% slower); experts dealt out in the order of their tiles' widths (1 to 2% slower); two
+// boxes of D per fence and store, or a second staging buffer (the 16 KB cost a stage of the ring: 0 to 11% slower).
 #pragma once
 
 #include "activation.cuh"
