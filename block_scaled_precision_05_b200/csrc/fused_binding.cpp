@@ -8,8 +8,10 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <string>
 
 #include "bsp.h"
@@ -190,10 +192,8 @@ PyObject* fused_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return run(c);
   } catch (const Refused& r) {
     PyErr_SetString(PyExc_ValueError, r.what.c_str());
-  } catch (const c10::Error& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own type for each of its errors: out of memory is torch.OutOfMemoryError, as from torch.empty
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
