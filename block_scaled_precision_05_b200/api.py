@@ -749,8 +749,12 @@ class NVFP4GroupedLinear:
 
     def __call__(self, x: torch.Tensor | None, offsets: torch.Tensor, pre_quantized: NVFP4Tensor | None = None,
                  out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
-        """x [M, K], or its quantized form as pre_quantized; offsets int32 [E + 1]."""
+        """x [M, K], or its quantized form as pre_quantized (per row for a per-token layer, else with a global scale of 1, as
+        quantize_input makes it); offsets int32 [E + 1]."""
         xq = pre_quantized if pre_quantized is not None else self.quantize_input(x)
+        if not self.per_token and xq.row_inv_gs is not None:
+            raise ValueError("pre_quantized has a scale for each row, and this layer's activation has one scale for all "
+                             "(per_token=False)")
         return nvfp4_grouped_gemm(xq, self.weight, offsets, self.alpha, xq.row_inv_gs if self.per_token else None,
                                   self.bias, out_dtype, out, self.activation, self.gated)
 

@@ -126,3 +126,17 @@ def test_interleave_gated():
     assert b.tolist() == [0, 10, 2, 12, 4, 14]
     with pytest.raises(ValueError):
         bsp.interleave_gated(g, u[:2])
+
+
+def test_grouped_layer_refuses_row_scales_it_would_leave_out():
+    """A layer with one activation scale has no use for the row scales of a per-token input: its result would lack them."""
+    layer = bsp.NVFP4GroupedLinear.__new__(bsp.NVFP4GroupedLinear)
+    layer.weight = bsp.NVFP4Experts(torch.zeros(2, 32, 32, dtype=torch.uint8), torch.zeros(2, 512, dtype=torch.uint8), 64)
+    layer.per_token, layer.activation, layer.gated, layer.alpha, layer.bias = False, None, False, torch.ones(2), None
+    off = torch.tensor([0, 1, 4], dtype=torch.int32)
+    xq = bsp.NVFP4Tensor(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 64, torch.ones(4), torch.ones(4))
+    with pytest.raises(ValueError, match="each row"):
+        layer(None, off, pre_quantized=xq)
+    layer.per_token = True
+    with pytest.raises(ValueError, match="CUDA"):  # taken as far as the binding's refusal of CPU tensors
+        layer(None, off, pre_quantized=xq)
