@@ -19,6 +19,7 @@ Sources (page title, then symbol):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -27,10 +28,17 @@ import torch
 from . import _native as nat
 
 
-def _stream(device: int | None = None) -> int:
-    """The current stream's handle, of the current device unless given.  The raw getter: a torch.cuda.Stream object
-    made for each launch takes 3 us."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if device is None else device)
+def _stream() -> int:
+    """The current stream's handle.  The raw getter: a torch.cuda.Stream object made for each launch takes 3 us."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Makes `device` the current one for a launch on its memory (a grouped layer's tokens may be on another)."""
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -197,11 +205,12 @@ def nvfp4_quantize(x: torch.Tensor, global_sf: torch.Tensor | None = None, per_r
         raise ValueError("out was allocated for another scale layout")
     if not per_row and global_sf is None:
         raise ValueError("per-tensor quantization needs global_sf (fp32 device tensor)")
-    st = nat.lib().nvfp4_quantize_ex(
-        _ptr(x2), nat.BSP_IN_BF16 if x2.dtype == torch.bfloat16 else nat.BSP_IN_F16, M, K, x2.stride(0),
-        None if per_row else _ptr(global_sf), nat.BSP_SF_PER_ROW if per_row else nat.BSP_SF_PER_TENSOR,
-        SF_LAYOUTS[sf_layout], _ptr(out.row_gs) if per_row else None, _ptr(out.row_inv_gs) if per_row else None,
-        _ptr(out.codes), _ptr(out.sf), _stream())
+    with _on(dev):
+        st = nat.lib().nvfp4_quantize_ex(
+            _ptr(x2), nat.BSP_IN_BF16 if x2.dtype == torch.bfloat16 else nat.BSP_IN_F16, M, K, x2.stride(0),
+            None if per_row else _ptr(global_sf), nat.BSP_SF_PER_ROW if per_row else nat.BSP_SF_PER_TENSOR,
+            SF_LAYOUTS[sf_layout], _ptr(out.row_gs) if per_row else None, _ptr(out.row_inv_gs) if per_row else None,
+            _ptr(out.codes), _ptr(out.sf), _stream())
     nat.check(st, "nvfp4_quantize_ex")
     return out
 
@@ -392,8 +401,9 @@ def mxfp8_quantize(x: torch.Tensor, out: MXFP8Tensor | None = None) -> MXFP8Tens
     if out is None:
         out = MXFP8Tensor(torch.empty((M, K), dtype=torch.uint8, device=dev),
                           torch.empty(mxfp8_sf_bytes(M, K), dtype=torch.uint8, device=dev), K)
-    nat.check(nat.lib().mxfp8_quantize(_ptr(x2), M, K, x2.stride(0), _ptr(out.q), _ptr(out.sf), _stream()),
-              "mxfp8_quantize")
+    with _on(dev):
+        st = nat.lib().mxfp8_quantize(_ptr(x2), M, K, x2.stride(0), _ptr(out.q), _ptr(out.sf), _stream())
+    nat.check(st, "mxfp8_quantize")
     return out
 
 

@@ -140,3 +140,54 @@ def test_grouped_layer_refuses_row_scales_it_would_leave_out():
     layer.per_token = True
     with pytest.raises(ValueError, match="CUDA"):  # taken as far as the binding's refusal of CPU tensors
         layer(None, off, pre_quantized=xq)
+
+
+class _Elsewhere:
+    """Stands for a tensor on cuda:1 while cuda:0 is current: what the quantizers ask of one, over CPU memory."""
+
+    def __init__(self, t, dtype=None):
+        self.t, self.dtype, self.is_cuda, self.device = t, dtype or t.dtype, True, torch.device("cuda", 1)
+        self.shape = t.shape
+
+    def reshape(self, *s):
+        return _Elsewhere(self.t.reshape(*s), self.dtype)
+
+    def stride(self, i):
+        return self.t.stride(i)
+
+    def data_ptr(self):
+        return self.t.data_ptr()
+
+    def is_floating_point(self):
+        return True
+
+
+def test_a_grouped_layers_tokens_on_another_device(monkeypatch):
+    """The layers quantize their tokens on the tokens' device and its stream, where the product runs too, not on the
+    current device."""
+    calls = []
+    current = [0]
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.d.index
+
+        def __exit__(self, *e):
+            current[0] = self.was
+
+    class Lib:
+        def __getattr__(self, name):
+            return (lambda *a: calls.append((name, current[0], a[-1])) or 0) if "quantize" in name else (lambda *a: 512)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 100 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(nat, "lib", lambda: Lib())
+    x = _Elsewhere(torch.zeros(4, 64, dtype=torch.bfloat16))
+    buf = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    api.nvfp4_quantize(x, _Elsewhere(torch.ones(1)), out=api.NVFP4Tensor(buf(4, 32), buf(512), 64))
+    api.mxfp8_quantize(x, out=api.MXFP8Tensor(buf(4, 64), buf(512), 64))
+    assert calls == [("nvfp4_quantize_ex", 1, 101), ("mxfp8_quantize", 1, 101)] and current == [0]
