@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "bsp.h"
+#include "per_device.h"
 
 namespace bsp {
 

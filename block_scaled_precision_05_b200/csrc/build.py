@@ -24,7 +24,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
 BINDING = os.path.join(PKG, "_fused_binding.so")
 SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "fused_gemm_nvfp4.cu", "fused_gemm_mxfp8.cu"]
-HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "fused_gemm.cuh", "norm_stats.cuh", "tensor_maps.h"]
+HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "fused_gemm.cuh", "norm_stats.cuh", "per_device.h",
+           "tensor_maps.h"]
 
 
 def nvcc() -> str:

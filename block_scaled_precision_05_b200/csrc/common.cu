@@ -11,7 +11,6 @@ __device__ uint32_t g_bsp_error_word;
 namespace bsp {
 
 namespace {
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices];
 }  // namespace

@@ -1013,11 +1013,11 @@ template <int KIND, int CG, bool kF32, bool kRes>
 int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cudaStream_t stream) {
   using C = FCfg<KIND, CG>;
   auto kernel = fused_gemm_kernel<KIND, CG, kF32, kRes>;
-  static bool attr_set[64] = {};
-  if (!attr_set[dev.id]) {
+  static PerDevice attr_set;
+  if (!attr_set.get(dev.id)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
       return launch_status();
-    attr_set[dev.id] = true;
+    attr_set.set(dev.id, 1);
   }
   FusedMaps maps;
   int st;
@@ -1068,14 +1068,13 @@ int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cud
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
-    static int resident[64][kMaxSplit + 1] = {};  // clusters resident at once, per device and size
-    int& r = resident[dev.id][cluster];
+    static PerDevice resident[kMaxSplit + 1];  // clusters resident at once, by size
+    int r = resident[cluster].get(dev.id);
     if (r == 0) {
       cfg.gridDim = dim3(static_cast<unsigned>(groups * cluster), 1, 1);
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return launch_status();
-      if (n < 1) return BSP_ERR_CUDA;  // a cluster does not fit: nothing launched
-      r = n;
+      if (cudaOccupancyMaxActiveClusters(&r, kernel, &cfg) != cudaSuccess) return launch_status();
+      if (r < 1) return BSP_ERR_CUDA;  // a cluster does not fit: nothing launched
+      resident[cluster].set(dev.id, r);
     }
     if (groups > r) groups = r;
     if (p.split > 1 && groups < most) {  // a split cluster takes one tile only

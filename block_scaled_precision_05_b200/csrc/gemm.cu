@@ -1055,11 +1055,11 @@ int launch_skinny(const DeviceInfo& dev, const uint8_t* A, const uint8_t* sfA, c
                   int64_t row_bytes, int64_t tiles_per_band, GemmParams p, cudaStream_t stream) {
   using C = SkCfg<KIND, BNA, kSf8, kSplit>;
   auto kernel = skinny_gemm_kernel<KIND, BNA, kSf8, kSplit>;
-  static bool attr_set[64] = {};
-  if (!attr_set[dev.id]) {
+  static PerDevice attr_set;
+  if (!attr_set.get(dev.id)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
       return launch_status();
-    attr_set[dev.id] = true;
+    attr_set.set(dev.id, 1);
   }
   CUtensorMap tmW, tmX, tmSFW, tmSFX;
   int st;
@@ -1146,11 +1146,11 @@ int launch_gemm(const DeviceInfo& dev, const uint8_t* A, const uint8_t* sfA, con
     return st;
   p.num_kb = static_cast<int>(ceil_div(row_bytes, C::ROW_BYTES));
   auto kernel = blockscaled_gemm_kernel<KIND, BN, CG>;
-  static bool attr_set[64] = {};
-  if (!attr_set[dev.id]) {
+  static PerDevice attr_set;
+  if (!attr_set.get(dev.id)) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess)
       return launch_status();
-    attr_set[dev.id] = true;
+    attr_set.set(dev.id, 1);
   }
   p.num_m = static_cast<int>(ceil_div(p.M, C::TILE_M));
   p.num_n = static_cast<int>(ceil_div(p.N, C::BN));
