@@ -119,9 +119,12 @@ def fused_gemm():
     global _fused_gemm
     if _fused_gemm is None:
         lib()
+        from .csrc import build
         try:
             from . import _fused_binding
-        except ImportError as e:
+            if _fused_binding.built_for != build.binding_target():
+                raise ImportError(f"built for {_fused_binding.built_for}, this is {build.binding_target()}")
+        except (ImportError, AttributeError) as e:
             raise RuntimeError("_fused_binding.so is missing or was built for another torch: build it with "
                                "`python -m block_scaled_precision_05_b200.csrc.build` (or __graft_entry__.build()). "
                                f"There is no fallback implementation. ({e})") from e

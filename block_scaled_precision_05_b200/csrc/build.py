@@ -23,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
 BINDING = os.path.join(PKG, "_fused_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "fused_binding.stamp")  # what BINDING was compiled against
 SOURCES = ["common.cu", "quantize.cu", "gemm.cu", "fused_gemm_nvfp4.cu", "fused_gemm_mxfp8.cu"]
 HEADERS = ["activation.cuh", "bsp_device.cuh", "bsp_internal.h", "fused_gemm.cuh", "norm_stats.cuh", "per_device.h",
            "tensor_maps.h"]
@@ -78,6 +79,21 @@ def _compile(src: str, verbose: bool, extra: list[str]) -> str:
     return obj
 
 
+def binding_target() -> str:
+    """The torch and Python that the binding is compiled against; the module holds it as `built_for`, and another torch or
+    Python gets a binding of its own."""
+    import torch
+
+    return f"torch {torch.__version__} cxx11abi={int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sys.implementation.cache_tag}"
+
+
+def _binding_stale(deps: list[str]) -> bool:
+    if _stale(BINDING, deps) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != binding_target()
+
+
 def _build_binding(verbose: bool) -> None:
     """csrc/fused_binding.cpp against torch's headers and libbsp.so (found next to it at run time)."""
     import sysconfig
@@ -85,13 +101,13 @@ def _build_binding(verbose: bool) -> None:
     import torch
 
     src = os.path.join(HERE, "fused_binding.cpp")
-    if not _stale(BINDING, [src, os.path.join(INCLUDE, "bsp.h"), os.path.abspath(__file__)]):
+    if not _binding_stale([src, os.path.join(INCLUDE, "bsp.h"), os.path.abspath(__file__)]):
         return
     top = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(cuda_lib_dir()), "include")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(top, "include"),
+           f'-DBSP_BUILT_FOR="{binding_target()}"', "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", os.path.join(top, "include"),
            "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-I", cuda, src, "-o", tmp,
            "-L", PKG, "-l:libbsp.so", "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
@@ -101,6 +117,8 @@ def _build_binding(verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for fused_binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(binding_target())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

@@ -207,4 +207,11 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fused_binding", nullptr, -1, kMe
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fused_binding() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__fused_binding() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", BSP_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
