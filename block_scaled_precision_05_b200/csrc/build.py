@@ -3,6 +3,10 @@ CPython binding of its fused GEMMs (_fused_binding.so, plain C++ over it).
 
     python -m block_scaled_precision_05_b200.csrc.build [--force] [--verbose]
 
+The library needs nvcc and its host compiler alone; without torch, Python's
+headers or g++ (run as a script: python block_scaled_precision_05_b200/csrc/build.py)
+it is built without the binding.
+
 Each .cu is compiled with nvcc (-gencode arch=compute_100a,code=sm_100a) in
 parallel into _build/, then linked against the shared CUDA runtime (so the
 library shares the process's runtime, device and streams with PyTorch).
@@ -11,10 +15,12 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
@@ -94,10 +100,23 @@ def _binding_stale(deps: list[str]) -> bool:
         return f.read() != binding_target()
 
 
+def binding_lacks() -> str | None:
+    """What the binding's build needs and this machine has not; the library does without it."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if shutil.which("g++") is None:
+        return "g++"
+    header = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return None if os.path.exists(header) else header
+
+
 def _build_binding(verbose: bool) -> None:
     """csrc/fused_binding.cpp against torch's headers and libbsp.so (found next to it at run time)."""
-    import sysconfig
-
+    lacks = binding_lacks()
+    if lacks is not None:
+        print(f"libbsp.so is built; _fused_binding.so (the Python binding of the fused GEMMs) is not: no {lacks}",
+              file=sys.stderr, flush=True)
+        return
     import torch
 
     src = os.path.join(HERE, "fused_binding.cpp")

@@ -52,3 +52,21 @@ def test_binding_in_place_is_this_torchs():
     assert os.path.exists(build.BINDING)
     nat.fused_gemm()
     assert sys.modules["block_scaled_precision_05_b200._fused_binding"].built_for == build.binding_target()
+
+
+@pytest.mark.parametrize("lacks", ["torch", "g++", "Python.h"])
+def test_library_builds_without_what_the_binding_needs(compiled, monkeypatch, capsys, tmp_path, lacks):
+    """libbsp.so is for C programs too: its build needs no torch, no Python headers and no g++."""
+    if lacks == "torch":
+        find = build.importlib.util.find_spec
+        monkeypatch.setattr(build.importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
+    elif lacks == "g++":
+        which = build.shutil.which
+        monkeypatch.setattr(build.shutil, "which", lambda n, *a, **k: None if n == "g++" else which(n, *a, **k))
+    else:
+        monkeypatch.setattr(build.sysconfig, "get_paths", lambda *a, **k: {"include": str(tmp_path / "none")})
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path / "build"))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libbsp.so"))
+    assert build.build() == build.LIB and os.path.exists(build.LIB)
+    assert not os.path.exists(build.BINDING) and lacks in capsys.readouterr().err
+    assert all("g++" not in c[0] for c in compiled)
