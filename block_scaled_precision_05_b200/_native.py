@@ -77,6 +77,7 @@ SIGNATURES = {
     "nvfp4_gemm_fused": (_i32, [_vp, _vp]),
     "mxfp8_gemm_fused": (_i32, [_vp, _vp]),
     "bsp_device_status": (_i32, [_vp]),
+    "bsp_debug_fused_plan": (_i32, [_i32, _i32, _i64, _i64, _i64, _i64, _i32, _vp]),
     "bsp_debug_encode_e2m1": (_i32, [_vp, _i64, _vp, _vp]),
     "bsp_debug_encode_e4m3": (_i32, [_vp, _i64, _vp, _vp]),
     "bsp_debug_wait_timeout": (_i32, [_i64, _vp]),

@@ -1002,8 +1002,8 @@ struct FusedArgs {
 // CTAs per tile: a split of K over a cluster when the tiles alone leave at least half of the SMs idle and every CTA
 // keeps at least kMinSplitSteps 128-byte steps.  Measured (us, split / whole): N = 5120, K = 13824 (54 steps), M = 16:
 // 14.6 / 18.3; N = 5120, K = 5120 (20 steps): two of 10 steps 11.5 / 10.9; N = 1536, K = 1536: 8.3 / 5.9.
-int fused_split(const DeviceInfo& dev, int64_t tiles, int num_kb) {
-  int64_t s = dev.sm_count / tiles;
+int fused_split(int sm_count, int64_t tiles, int64_t num_kb) {
+  int64_t s = sm_count / tiles;
   s = s < kMaxSplit ? s : kMaxSplit;
   s = s < num_kb / kMinSplitSteps ? s : num_kb / kMinSplitSteps;
   return s < 1 ? 1 : static_cast<int>(s);
@@ -1037,17 +1037,12 @@ int launch_variant(const DeviceInfo& dev, const FusedArgs& a, FusedParams p, cud
 
   p.num_kb = static_cast<int>(ceil_div(a.row_bytes, 128));
   p.panels = static_cast<int>(ceil_div(p.N, 128 * CG));
-  int64_t groups = dev.sm_count / CG;
-  p.split = 1;
+  int64_t groups = dev.sm_count / CG / p.split;
   if constexpr (CG == 1) {
     p.x_bytes = static_cast<int>(round_up(p.tn, 32)) * 128;
     p.stage_bytes = static_cast<int>(round_up(C::W_BYTES + p.x_bytes + C::BAND_BYTES * (1 + C::X_BANDS), 1024));
     p.stages = C::RING_BYTES / p.stage_bytes;
     if (p.stages > C::MAX_STAGES) p.stages = C::MAX_STAGES;
-    if (p.offsets == nullptr) {
-      p.split = fused_split(dev, ceil_div(p.M, p.tn) * p.panels, p.num_kb);
-      groups /= p.split;
-    }
   }
   const int64_t most = (ceil_div(p.M, p.tn) + (p.offsets == nullptr ? 0 : p.E < p.M ? p.E : p.M)) * p.panels;
   if (most > (1ll << 30)) return BSP_ERR_INVALID_ARG;  // tiles, at most
@@ -1119,25 +1114,25 @@ int launch_fused(const DeviceInfo& dev, const FusedArgs& a, const FusedParams& p
 //    smallest whose tiles fit in one wave (M = 256, N = K = 1536: 6.9 against 7.4 at 128).  Experts: 32 up to a mean
 //    of 8 rows, 64 up to 24 (128 experts of 1536 x 2048, tiles of 32 / 64 / 128: 39.9 / 40.6 / 41.4 at 8 rows, 41.8 /
 //    39.7 / 40.9 at 16, 53.1 / 43.3 / 41.1 at 32).
-bool choose_tile(const DeviceInfo& dev, FusedParams& p, int64_t num_kb) {
-  const int64_t panels = ceil_div(p.N, 128), waves = num_kb <= 8 ? 3 : 1;
-  if (p.offsets == nullptr) {
-    if (ceil_div(p.M, 128) * panels > waves * dev.sm_count) {
-      p.tn = 256;
-      return true;
-    }
-    for (p.tn = 32; p.tn < 128; p.tn *= 2)
-      if (p.M <= p.tn || (num_kb <= 8 && ceil_div(p.M, p.tn) * panels <= dev.sm_count)) break;
-    return false;
+struct FusedPlan {
+  int ctas;   // 2: CTA pairs
+  int tn;     // token tile
+  int split;  // CTAs of a cluster sharing a tile's K range
+};
+
+FusedPlan plan_fused(int sm_count, bool grouped, int64_t E, int64_t M, int64_t N, int64_t num_kb) {
+  const int64_t panels = ceil_div(N, 128), waves = num_kb <= 8 ? 3 : 1;
+  if (!grouped) {
+    if (ceil_div(M, 128) * panels > waves * sm_count) return {2, 256, 1};
+    int tn = 32;
+    for (; tn < 128; tn *= 2)
+      if (M <= tn || (num_kb <= 8 && ceil_div(M, tn) * panels <= sm_count)) break;
+    return {1, tn, fused_split(sm_count, ceil_div(M, tn) * panels, num_kb)};
   }
-  const int64_t rows = ceil_div(p.M, p.E);
-  const int64_t single = (2 * ceil_div(p.M, 128) + p.E) * panels;  // twice the single tiles, about
-  if (rows > (num_kb <= 4 ? 160 : 64) && single > 7 * dev.sm_count) {
-    p.tn = 256;
-    return true;
-  }
-  p.tn = rows <= 8 ? 32 : rows <= 24 ? 64 : 128;
-  return false;
+  const int64_t rows = ceil_div(M, E);
+  const int64_t single = (2 * ceil_div(M, 128) + E) * panels;  // twice the single tiles, about
+  if (rows > (num_kb <= 4 ? 160 : 64) && single > 7 * sm_count) return {2, 256, 1};
+  return {1, rows <= 8 ? 32 : rows <= 24 ? 64 : 128, 1};
 }
 
 template <int KIND>
@@ -1188,8 +1183,10 @@ int run_fused(const bsp_fused_gemm_desc* d, cudaStream_t stream) {
   p.ld_d = d->ld_d;
   p.err = dev.err_word;
   const bool f32 = d->d_dtype == BSP_OUT_F32;
-  const bool pairs = choose_tile(dev, p, ceil_div(a.row_bytes, 128));
-  return pairs ? launch_fused<KIND, 2>(dev, a, p, f32, stream) : launch_fused<KIND, 1>(dev, a, p, f32, stream);
+  const FusedPlan plan = plan_fused(dev.sm_count, p.offsets != nullptr, E, M, N, ceil_div(a.row_bytes, 128));
+  p.tn = plan.tn;
+  p.split = plan.split;
+  return plan.ctas == 2 ? launch_fused<KIND, 2>(dev, a, p, f32, stream) : launch_fused<KIND, 1>(dev, a, p, f32, stream);
 }
 
 }  // namespace

@@ -506,6 +506,11 @@ int bsp_device_status(bsp_stream_t stream);
 int bsp_debug_encode_e2m1(const float *v, int64_t n, uint8_t *codes, bsp_stream_t stream);
 /* bytes[i] = e4m3 byte of v[i] by the kernels' conversion path. */
 int bsp_debug_encode_e4m3(const float *v, int64_t n, uint8_t *bytes, bsp_stream_t stream);
+/* What nvfp4_gemm_fused (mxfp8 != 0: mxfp8_gemm_fused) chooses for these sizes on a device of sm_count SMs: plan (HOST
+ * memory, 3 words) receives the CTAs that share a tile's rows (2: a CTA pair), the most rows of A in a tile, and the CTAs
+ * of a cluster that share its K range (1 where the device cannot hold as many clusters at once as there are tiles).
+ * Needs no device. */
+int bsp_debug_fused_plan(int mxfp8, int grouped, int64_t E, int64_t M, int64_t N, int64_t K, int sm_count, int32_t *plan);
 /* Launches one block that waits on a shared-memory barrier nobody arrives at,
  * with a limit of `limit_ns` nanoseconds (1e3 .. 1e10).  The wait runs out and
  * sets the error word, so bsp_device_status then returns BSP_ERR_TIMEOUT. */

@@ -191,3 +191,36 @@ def test_a_grouped_layers_tokens_on_another_device(monkeypatch):
     api.nvfp4_quantize(x, _Elsewhere(torch.ones(1)), out=api.NVFP4Tensor(buf(4, 32), buf(512), 64))
     api.mxfp8_quantize(x, out=api.MXFP8Tensor(buf(4, 64), buf(512), 64))
     assert calls == [("nvfp4_quantize_ex", 1, 101), ("mxfp8_quantize", 1, 101)] and current == [0]
+
+
+def test_plan_of_the_sizes():
+    """The form a call takes, at both sides of each border of the rules (148 SMs)."""
+    import ctypes
+
+    def plan(mxfp8, E, M, N, K, sms=148):
+        out = (ctypes.c_int32 * 3)()
+        assert nat.lib().bsp_debug_fused_plan(mxfp8, int(E > 0), max(E, 1), M, N, K, sms, ctypes.addressof(out)) == nat.BSP_OK
+        return tuple(out)
+
+    pair = (2, 256, 1)
+    # dense: pairs once the 128 x 128 tiles exceed one wave, three waves up to 8 steps of 128 bytes
+    assert plan(0, 0, 128, 148 * 128, 2080) == (1, 128, 1) and plan(0, 0, 128, 148 * 128 + 8, 2080) == pair
+    assert plan(0, 0, 1, 148 * 128 + 8, 2080) == pair and plan(0, 0, 1, 148 * 128 + 8, 2048)[0] == 1
+    assert plan(0, 0, 128, 444 * 128, 2048) == (1, 128, 1) and plan(0, 0, 129, 222 * 128 + 8, 2048) == pair
+    assert plan(1, 0, 128, 148 * 128 + 8, 1056) == pair and plan(1, 0, 128, 148 * 128 + 8, 1024) == (1, 128, 1)
+    # token tiles of single CTAs
+    assert [plan(0, 0, m, 1024, 2080)[1] for m in (1, 32, 33, 64, 65, 128, 500)] == [32, 32, 64, 64, 128, 128, 128]
+    assert plan(0, 0, 256, 1536, 1536) == (1, 32, 1) and plan(0, 0, 512, 1536, 1536) == (1, 64, 1)
+    # split K: 16 steps a CTA at least, 4 CTAs at most, no more than the SMs hold
+    assert [plan(0, 0, 1, 1024, 256 * s)[2] for s in (31, 32, 47, 48, 63, 64, 200)] == [1, 2, 2, 3, 3, 4, 4]
+    assert [plan(0, 0, 1, 128 * p, 256 * 64)[2] for p in (37, 38, 49, 50, 74, 75)] == [4, 3, 3, 2, 2, 1]
+    # experts: pairs above a mean of 64 rows (160 up to 4 steps) and about 3.5 waves; never split
+    assert plan(0, 4, 256, 128 * 200, 1312) == (1, 128, 1) and plan(0, 4, 257, 128 * 200, 1312) == pair
+    assert plan(0, 4, 640, 128 * 200, 1024) == (1, 128, 1) and plan(0, 4, 641, 128 * 200, 1024) == pair
+    assert plan(0, 8, 1152, 128 * 39, 1312) == (1, 128, 1) and plan(0, 8, 1152, 128 * 40, 1312) == pair
+    assert [plan(0, 4, 4 * m, 1024, 16384)[1:] for m in (1, 8, 9, 24, 25, 64)] == [(32, 1), (32, 1), (64, 1), (64, 1), (128, 1), (128, 1)]
+    plan_of = nat.lib().bsp_debug_fused_plan
+    buf = ctypes.addressof((ctypes.c_int32 * 3)())
+    for bad in ((0, 0, 1, 0, 8, 32, 148, buf), (0, 0, 1, 1, 0, 32, 148, buf), (0, 0, 1, 1, 8, 48, 148, buf),
+                (0, 0, 0, 1, 8, 32, 148, buf), (0, 0, 1, 1, 8, 32, 0, buf), (0, 0, 1, 1, 8, 32, 148, None)):
+        assert plan_of(*bad) == nat.BSP_ERR_INVALID_ARG
