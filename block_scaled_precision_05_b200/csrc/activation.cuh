@@ -1,9 +1,10 @@
 // activation.cuh -- the activations of the fused GEMM epilogues, on fp32 values, two at a time.
 //
-// exp2 and the reciprocal are the hardware approximations (2^-22 relative error each, documented by PTX), so an
-// activation is within about 1e-6 of its formula relative to the result, far below half a step of bf16 (2^-9), and
-// below the rounding noise of an fp32 sum over K.  Tails keep their relative accuracy: nothing is computed as
-// 1 + tanh(x) or 1 + erf(x), which cancel for negative x.
+// exp2 and the reciprocal are the hardware approximations (2^-22 relative error each, documented by PTX), and the
+// exponent s of 2^s is rounded to fp32, which is worth up to 2^-23 |s| of the exponential.  So an activation is within
+// (|s| + 6) 2^-22 of its formula relative to the result: 2e-6 for |x| <= 1, at most 3.2e-5 at the end of the tail,
+// |s| = 126, far below half a step of bf16 (2^-9).  Nothing is computed as 1 + tanh(x) or 1 + erf(x), which cancel for
+// negative x.  Where 2^s is below the smallest normal number it is 0: a tail ends at magnitudes below 1.1e-36.
 //
 // Both run on the special-function unit, 4 lanes a clock in each SM quarter, and an epilogue that applies an
 // activation is bound by it.  So two values share one reciprocal: 1/p = q / (pq), 1/q = p / (pq).
@@ -34,28 +35,31 @@ __device__ __forceinline__ float max_nan(float x, float c) {
   return y;
 }
 
-// x / (1 + 2^e(x)) for both, e(x) <= 60 so that the product of the denominators stays in range.  The minimum takes
-// nothing but a NaN, which must not reach the other value through the shared reciprocal: x itself keeps it.
-__device__ __forceinline__ void logistic2(float& x0, float& x1, float e0, float e1) {
-  const float p = 1.0f + ex2_approx(fminf(e0, 60.0f)), q = 1.0f + ex2_approx(fminf(e1, 60.0f));
+// x / (1 + 2^-s) for both, s of x's sign, from t = 2^-|s| <= 1: x / (1 + t), and x t / (1 + t) where x < 0, so that
+// nothing overflows and the tail of negative x is t's own, down to where t is below the smallest normal number (then
+// -0).  The minimum takes nothing but a NaN, which must not reach the other value through the shared reciprocal: x
+// itself keeps it.
+__device__ __forceinline__ void logistic2(float& x0, float& x1, float s0, float s1) {
+  const float t0 = fminf(ex2_approx(-fabsf(s0)), 1.0f), t1 = fminf(ex2_approx(-fabsf(s1)), 1.0f);
+  const float p = 1.0f + t0, q = 1.0f + t1;
   const float r = rcp_approx(p * q);
-  x0 *= r * q;
-  x1 *= r * p;
+  x0 *= (x0 < 0.0f ? t0 : 1.0f) * (r * q);
+  x1 *= (x1 < 0.0f ? t1 : 1.0f) * (r * p);
 }
 
-// x / (1 + e^-x); below -40 as at -40 (-1.7e-16).
+// x / (1 + e^-x).  The maximum is for -infinity times a t of 0; at -1000 t has long been 0.
 __device__ __forceinline__ void silu2(float& x0, float& x1) {
-  x0 = max_nan(x0, -40.0f);
-  x1 = max_nan(x1, -40.0f);
-  logistic2(x0, x1, -1.44269504f * x0, -1.44269504f * x1);
+  x0 = max_nan(x0, -1000.0f);
+  x1 = max_nan(x1, -1000.0f);
+  logistic2(x0, x1, 1.44269504f * x0, 1.44269504f * x1);
 }
 
 // x/2 (1 + tanh u) = x / (1 + e^-2u), u = sqrt(2/pi) (x + 0.044715 x^3); the constants are 2 sqrt(2/pi) log2(e) and
-// that times 0.044715.  Below -7 as at -7 (-2.3e-15).
+// that times 0.044715.  The maximum as in silu2.
 __device__ __forceinline__ void gelu_tanh2(float& x0, float& x1) {
-  x0 = max_nan(x0, -7.0f);
-  x1 = max_nan(x1, -7.0f);
-  logistic2(x0, x1, -x0 * fmaf(0.102943240f, x0 * x0, 2.30220820f), -x1 * fmaf(0.102943240f, x1 * x1, 2.30220820f));
+  x0 = max_nan(x0, -1000.0f);
+  x1 = max_nan(x1, -1000.0f);
+  logistic2(x0, x1, x0 * fmaf(0.102943240f, x0 * x0, 2.30220820f), x1 * fmaf(0.102943240f, x1 * x1, 2.30220820f));
 }
 
 // x Phi(x) = max(x, 0) - |x| Q(|x|) with the normal tail Q(u) = e^(-u^2/2) P(1 / (1 + 0.23 u)).  P is a polynomial of
