@@ -1231,8 +1231,9 @@ int run_gemm(const uint8_t* A, const uint8_t* sfA, const uint8_t* B, const uint8
   const bool skinny = M <= BSP_GEMM_SKINNY_MAX_M;
   const int64_t row_bytes = KIND == kNVF4 ? K / 2 : K;
   const int64_t tiles_per_band = round_up(K / group, 4) / 4;
-  CUtensorMap tmD;
-  if ((st = encode_output(&tmD, D, M, N, ld_d, d_dtype == BSP_OUT_F32)) != BSP_OK) return st;
+  CUtensorMap tmD;  // boxes of 32 rows x 32 bytes
+  const bool f32 = d_dtype == BSP_OUT_F32;
+  if ((st = encode_rows(&tmD, D, M, N, ld_d, f32, 32, f32 ? 8 : 16)) != BSP_OK) return st;
 
   GemmParams p;
   p.M = static_cast<int>(M);

@@ -48,19 +48,6 @@ inline int encode_scales(CUtensorMap* m, const void* base, int64_t bands, int64_
   return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
 }
 
-// Row-major output [rows, ld] of bf16 or fp32, boxes of 32 rows x 32 bytes, 32-byte swizzle.
-inline int encode_output(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
-  const int64_t esize = f32 ? 4 : 2;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * esize)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(32 / esize), 32u};
-  cuuint32_t es[2] = {1u, 1u};
-  CUresult r = encode_tiled_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
-                                 dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
-                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_INVALID_ARG;
-}
-
 // Row-major output [rows, ld] of bf16 or fp32, boxes of box_rows rows x box_cols columns (32, 64 or 128 bytes, with
 // the swizzle of that width).
 inline int encode_rows(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32, int box_rows,
