@@ -85,14 +85,12 @@ def _code_only(src: str) -> str:
     return " ".join("".join(out).split())
 
 
-# the sources each timed kernel is compiled from (its own file and the shared headers)
+# the sources each timed kernel is compiled from (its own file and the headers it takes)
+_SHARED = ("bsp_device.cuh", "bsp_internal.h", "per_device.h")
 KERNEL_SOURCES = {
-    "nvfp4_gemm": ("gemm.cu", "bsp_device.cuh", "bsp_internal.h"),
-    "mxfp8_gemm": ("gemm.cu", "bsp_device.cuh", "bsp_internal.h"),
-    "nvfp4_quantize": ("quantize.cu", "bsp_device.cuh", "bsp_internal.h", "norm_stats.cuh"),
-    "nvfp4_rmsnorm_quantize": ("quantize.cu", "bsp_device.cuh", "bsp_internal.h", "norm_stats.cuh"),
-    "nvfp4_layernorm_quantize": ("quantize.cu", "bsp_device.cuh", "bsp_internal.h", "norm_stats.cuh"),
-    "mxfp8_quantize": ("quantize.cu", "bsp_device.cuh", "bsp_internal.h", "norm_stats.cuh"),
+    **dict.fromkeys(("nvfp4_gemm", "mxfp8_gemm"), ("gemm.cu", *_SHARED, "tensor_maps.h")),
+    **dict.fromkeys(("nvfp4_quantize", "nvfp4_rmsnorm_quantize", "nvfp4_layernorm_quantize", "mxfp8_quantize"),
+                    ("quantize.cu", *_SHARED, "norm_stats.cuh")),
 }
 
 

@@ -40,3 +40,28 @@ def test_traffic_entries_are_keyed_to_their_kernels_sources():
         for kernel, e in entries.items():
             assert tuple(e["sources"]) == bench.KERNEL_SOURCES[kernel]
             assert abs(e["read"] + e["write"] - e["dram_bytes_per_launch"]) <= 1  # each averaged, then truncated
+
+
+def test_every_traffic_entry_is_of_the_present_sources():
+    """A capture of other sources would drop out of the bench's roofline without a word: it is taken again instead."""
+    import json
+    import os
+    with open(os.path.join(bench.ROOT, "profiles", "traffic.json")) as f:
+        t = json.load(f)
+    stale = [(w, k) for w, entries in t.items() if not w.startswith("_") for k in entries if bench.traffic_for(k, w) is None]
+    assert not stale, stale
+
+
+def test_kernel_sources_name_every_header():
+    """The headers that a kernel's source takes, directly or through one of them, are part of its hash."""
+    import os
+    import re
+    csrc = os.path.join(bench.ROOT, "block_scaled_precision_05_b200", "csrc")
+    for kernel, names in bench.KERNEL_SOURCES.items():
+        todo, seen = [names[0]], set()
+        while todo:
+            seen.add(todo[-1])
+            for h in re.findall(r'#include "([^"]+)"', open(os.path.join(csrc, todo.pop())).read()):
+                if h not in seen and os.path.exists(os.path.join(csrc, h)):
+                    todo.append(h)
+        assert seen == set(names), kernel
