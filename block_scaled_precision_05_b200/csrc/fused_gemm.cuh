@@ -22,17 +22,23 @@
 // 8-15 are the epilogue.  Every CTA builds the table of the experts' tiles in shared memory from the offsets (a scan
 // over the experts) and takes every gridDim-th tile: nothing is read back to the host.
 //
-// What bounds it, measured on one B200:
+// What bounds it, measured on one B200 (launches back to back on the same operands; a pass whose operands come from DRAM
+// after others in brackets):
 //  - large products: operand delivery and power.  A 256 x 256 tile of a pair takes 38 KB per SM and K step; the ring
 //    runs at 548 clocks a step without MMAs (70 bytes a clock and SM from L2), 615 with them (an ideal of 514), at the
-//    1.35 to 1.4 GHz that the 1000 W cap leaves: 32760 x 13824 x 5120 868 us (bias-free), 5340 TFLOP/s.
+//    1.35 to 1.4 GHz that the 1000 W cap leaves: 32760 x 13824 x 5120 868 us in short bursts without a bias, 1033 over a
+//    second with bias and relu [1077 with gelu_tanh].
 //  - experts of a few hundred rows: per tile, the hand-over of the one 256-column accumulator (last MMA to first MMA of
 //    the next tile, about 3000 clocks) beside 8 K steps of 520 to 600 clocks: 128 experts, 32768 rows, 1536 x 2048 gated
-//    81 us.  Two 128-column accumulators instead (no hand-over, twice the weight traffic): 112 us.
+//    81 to 86 us [97].  Two 128-column accumulators instead (no hand-over, twice the weight traffic): 112 us.
 //  - short K: the epilogue, about 900 clocks per warp for 32 tokens x 32 columns (200 of arithmetic, then one after
 //    another the buffer's wait, the turn through shared memory, the fence and the store), plus 8 to 12 clocks of the
-//    special-function unit for each activated value: 128 experts, 32768 x 2048 x 768 59 us, without it 43.
-//  - decoding batches: the weight stream; 512 rows over 117 of 128 experts of 1536 x 2048, 208 MB in 34.4 us, 6.05 TB/s.
+//    special-function unit for each activated value: 128 experts, 32768 x 2048 x 768 59 to 64 us, without it 43 [72];
+//    32760 x 1536 x 1536 44 us with relu, 65 with gelu_tanh, 59 to 63 with silu, 80 with gelu, 74 with a residual.
+//  - decoding batches: the weight stream; 512 rows over 117 of 128 experts of 1536 x 2048, 208 MB in 34 to 39 us [40].
+//  - registers: with a residual, in fp32, or both, the epilogue spills where it has the accumulator in registers (-Xptxas
+//    -v, bytes stored / loaded a thread: pairs 116 / 248 with a bf16 residual, 44 / 168 in fp32, 40 / 164 in fp32 with a
+//    residual; single CTAs 20 / 72 at most).
 // Not kept: an L2 prefetch of the next tile's weights (3 to 12% slower); the follower's warps arriving on the leader's
 // barriers themselves (2 to 10% slower); experts dealt out in the order of their tiles' widths (1 to 2% slower); two
 // boxes of D per fence and store, or a second staging buffer (the 16 KB cost a stage of the ring: 0 to 11% slower).
@@ -1099,7 +1105,9 @@ int launch_fused(const DeviceInfo& dev, const FusedArgs& a, const FusedParams& p
                     : launch_variant<KIND, CG, false, false>(dev, a, p, stream);
 }
 
-// The form and the token tile, from the sizes and the experts' mean row count (their own are on the device).
+// The form and the token tile, from the sizes and the experts' mean row count (their own are on the device; with a buffer
+// taller than its live rows the mean is too high: 512 rows over 128 experts of 1536 x 2048 in a buffer of 32768 rows take
+// pairs, 46.6 us against 41.5 in an exact one, 8192 rows 49.9 against 47.9).
 //  - CTA pairs (256 x 256 tiles) once the 128 x 128 tiles of single CTAs no longer fit in one wave: the pair's operands
 //    cost half the bandwidth (us, pairs / single: M = 4096, N = 13824, K = 5120: 121 / 162; M = 256, same weights:
 //    18.2 / 20.5), but its epilogue and its larger tiles take longer where everything runs at once (M = 256, N = 5120,

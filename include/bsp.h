@@ -460,7 +460,9 @@ int mxfp8_gemm(const uint8_t *A, const uint8_t *sfA, const uint8_t *B, const uin
  *               bsp_mxfp8_sf_bytes(N, K) bytes one after another
  *   offsets   : int32 [E + 1] or NULL (E = 1).  Values outside [0, M] are
  *               clamped, and one below an earlier one counts as that one.  An
- *               expert may have no row.
+ *               expert may have no row.  They stay on the device: the kernel's
+ *               form is chosen from M / E, so a buffer much taller than its live
+ *               rows may cost some percent (13% at most measured).
  *   alpha     : fp32 [E] or NULL (1)
  *   row_scale : fp32 [M] or NULL; NULL for MXFP8
  *   bias      : bf16 [E, N] or NULL
